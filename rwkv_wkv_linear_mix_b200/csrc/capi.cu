@@ -10,6 +10,7 @@
 
 #include <mutex>
 
+#include "ssm_internal.h"
 #include "wkv.h"
 #include "wkv_internal.h"
 
@@ -91,6 +92,8 @@ wkv_status check_act(int64_t B, int64_t T, int64_t C, int dtype) {
 }  // namespace
 
 void set_last_error(const char* why) { t_last_error = why ? why : ""; }
+
+wkv_status device_error_word(unsigned** out) { return device_error_ptr(out); }
 
 bool encode_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, size_t elem_bytes, uint64_t d0,
                     uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2, const char** why,

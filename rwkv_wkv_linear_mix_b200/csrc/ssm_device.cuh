@@ -1,0 +1,151 @@
+// ssm_device.cuh -- device-side building blocks of the state-space operators:
+// vectors of N elements as stored, the logistic and softplus functions, and
+// sums over lanes that leave each lane its share of the results.
+#pragma once
+
+#include "ssm_internal.h"
+#include "wkv_device.cuh"
+
+namespace wkv {
+
+// N consecutive elements of E as loaded (packed); N * sizeof(E) is 4, 8, 16 or 32 bytes.
+template <class E, int N>
+struct Pack {
+  static constexpr int kBytes = N * (int)sizeof(E);
+  static constexpr int kWords = kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = q.x;
+        w[4 * i + 1] = q.y;
+        w[4 * i + 2] = q.z;
+        w[4 * i + 3] = q.w;
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x;
+      w[1] = q.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        f[2 * i] = bf16lo(w[i]);
+        f[2 * i + 1] = bf16hi(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[N]) {
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __float_as_uint(f[i]);
+    }
+  }
+};
+
+// N float32 parameters (16-byte aligned), or a constant where there are none.
+template <int N>
+__device__ __forceinline__ void ld_param(const float* p, float (&f)[N], float otherwise) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = otherwise;
+  if (p) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      f[i] = q.x;
+      f[i + 1] = q.y;
+      f[i + 2] = q.z;
+      f[i + 3] = q.w;
+    }
+  }
+}
+
+// sigmoid(x) = 1 / (1 + e^-x). e^-x overflows to inf below -88, whose
+// reciprocal is the right 0.
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp(__fadd_rn(1.f, ex2(__fmul_rn(x, -kLog2e)))); }
+
+// softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| <= 1, and its
+// derivative sigmoid(x). log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
+// the series of atanh (the first term left out is below 1.5e-8 of the sum):
+// it keeps its relative precision where e is small, which log(1 + e) loses.
+__device__ __forceinline__ float softplus_f(float x) {
+  const float e = ex2(__fmul_rn(fabsf(x), -kLog2e));
+  const float s = __fmul_rn(e, rcp(__fadd_rn(2.f, e)));
+  const float q = __fmul_rn(s, s);
+  float p = 1.f / 13.f;
+  p = __fmaf_rn(p, q, 1.f / 11.f);
+  p = __fmaf_rn(p, q, 1.f / 9.f);
+  p = __fmaf_rn(p, q, 1.f / 7.f);
+  p = __fmaf_rn(p, q, 1.f / 5.f);
+  p = __fmaf_rn(p, q, 1.f / 3.f);
+  p = __fmaf_rn(p, q, 1.f);
+  return __fmaf_rn(__fadd_rn(s, s), p, fmaxf(x, 0.f));
+}
+
+// Sums of NV values over the NL lanes that differ in the lane bits
+// BIT .. BIT * NL / 2, in halving steps: each step sends half of the values
+// away and adds the other lane's half, so that NL lanes end with NV / NL sums
+// each (or, with NV < NL, with copies of one). Lane bit b of the NL chooses
+// the upper half in step b, i.e. the first result of a lane is value
+// reduce_scatter_first<NV, NL>(lane / BIT % NL). The partner lanes, and so
+// the rounding, are the same for every NV.
+template <int NV, int NL, int BIT = 1>
+__device__ __forceinline__ void reduce_scatter(float (&v)[NV], int lane) {
+  if constexpr (NL > 1) {
+    if constexpr (NV > 1) {
+      const bool up = lane & BIT;
+      float r[NV / 2];
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) {
+        const float send = up ? v[i] : v[i + NV / 2];
+        const float keep = up ? v[i + NV / 2] : v[i];
+        r[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, BIT));
+      }
+      reduce_scatter<NV / 2, NL / 2, BIT * 2>(r, lane);
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) v[i] = r[i];
+    } else {
+      v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], BIT));
+      reduce_scatter<1, NL / 2, BIT * 2>(v, lane);
+    }
+  }
+}
+template <int NV, int NL>
+__device__ __forceinline__ int reduce_scatter_first(int l) {
+  int first = 0, half = NV / 2;
+#pragma unroll
+  for (int b = 1; b < NL; b *= 2) {
+    if (half >= 1 && (l & b)) first += half;
+    half /= 2;
+  }
+  return first;
+}
+
+}  // namespace wkv

@@ -1,0 +1,132 @@
+// ssm_internal.h -- host-side interface between the C ABI layer of the
+// state-space operators (ssm_capi.cu) and their kernel launchers.
+#pragma once
+
+#include "wkv_internal.h"
+#include "wkv_ssm.h"
+
+namespace wkv {
+
+// Address of the current device's error word (capi.cu).
+wkv_status device_error_word(unsigned** out);
+
+// out[i][c] = sum over the rows of part[i][rows][cols], in a fixed order.
+wkv_status launch_sum_rows(const float* part, int planes, int64_t rows, int64_t cols, float* out, cudaStream_t stream,
+                           const char** why);
+
+// ---- short causal convolution ------------------------------------------------
+struct ConvArgs {
+  int64_t B, T, C;  // slots: B = S, T unused
+  int dtype, W, silu;
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const void* x_prev;
+  void* y;
+  const void* gy;
+  void* gx;
+  float* gweight;
+  float* gbias;
+  void* gx_prev;
+  float* part;
+  int64_t n_tokens;
+  const int32_t* cu;
+  void* state;
+};
+// Launch shape: channel blocks, and each sequence cut into nrun runs of Lt tokens.
+struct ConvShape {
+  int ncb, nrun, Lt;
+};
+ConvShape conv_bwd_shape(int64_t B, int64_t T, int64_t C);
+wkv_status launch_conv_forward(const ConvArgs& a, cudaStream_t stream, const char** why);
+wkv_status launch_conv_backward(const ConvArgs& a, cudaStream_t stream, const char** why);
+wkv_status launch_conv_chunk_step(const ConvArgs& a, cudaStream_t stream, unsigned* err, const char** why);
+wkv_status launch_conv_decode_step(const ConvArgs& a, cudaStream_t stream, const char** why);
+
+// ---- per-head norm with rotation ------------------------------------------------
+struct NormArgs {
+  int64_t tokens, T;  // tokens = B * T
+  int Hq, Hk, K, R, dtype, interleaved;
+  const void* q;
+  const void* k;
+  const float* wq;
+  const float* wk;
+  float eps;
+  const float* inv_freq;
+  const int32_t* positions;
+  int64_t pos_offset;
+  void* q_out;  // backward: gq
+  void* k_out;  // backward: gk
+  const void* gq;
+  const void* gk;
+  float* gwq;
+  float* gwk;
+  float* part;
+};
+// CTAs of the backward kernel (each leaves one row of weight-gradient partial sums).
+int64_t norm_bwd_blocks(int64_t tokens, int64_t Hq, int64_t Hk, int64_t K);
+wkv_status launch_norm_rotate(const NormArgs& a, cudaStream_t stream, const char** why);
+wkv_status launch_norm_rotate_backward(const NormArgs& a, cudaStream_t stream, const char** why);
+
+// ---- selective scan -------------------------------------------------------------
+struct ScanArgs {
+  int64_t B, T, C, N, G;  // slots: B = S, T unused
+  int dtype;
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* D;
+  const void* z;
+  const float* dt_bias;
+  int softplus;
+  const float* init_state;
+  void* y;
+  float* final_state;
+  float* ckpt;
+  float* carry;  // pieces of a cut sequence: [B][nseg][C][N] states, then [B][nseg][C] sums of d
+  int64_t n_tokens;
+  const int32_t* cu;  // slots, else null
+};
+struct ScanBwdArgs {
+  ScanArgs f;  // f.ckpt: the checkpoints (read); f.carry: pieces of the reverse walk
+  const void* gy;
+  const float* g_final;
+  void* gx;
+  void* gdt;
+  float* gA;
+  void* gB;
+  void* gC;
+  float* gD;
+  void* gz;
+  float* gdt_bias;
+  float* g_init;
+  float* part_bc;  // [2][blocks per group][B*T][G*N]
+  float* part_a;   // [B*nseg][C][N]
+  float* part_d;   // [2][B*nseg][C]: gD, gdt_bias
+};
+// Lanes that share a channel (4 states each): 2, 4, 8 or 16.
+inline int scan_lanes(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+// Channels per CTA.
+inline int scan_block_channels(int64_t N) { return std::min(64, 256 / scan_lanes(N)); }
+// CTAs that cover one group's channels.
+inline int64_t scan_group_blocks(int64_t C, int64_t N, int64_t G) {
+  return ceil_div(C / std::max<int64_t>(G, 1), scan_block_channels(N));
+}
+// Pieces along T (1: uncut) of the forward and of the backward; each but the
+// last has seg_tiles * WKV_SCAN_CKPT_LEN tokens.
+struct ScanCut {
+  int nseg, seg_tiles;
+};
+ScanCut scan_fwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G);
+ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G);
+inline int64_t scan_carry_floats(int64_t B, int64_t C, int64_t N, int nseg) {
+  return nseg > 1 ? B * nseg * C * (N + 1) : 0;
+}
+wkv_status launch_scan_forward(const ScanArgs& a, cudaStream_t stream, const char** why);
+wkv_status launch_scan_chunk_step(const ScanArgs& a, cudaStream_t stream, unsigned* err, const char** why);
+wkv_status launch_scan_decode_step(const ScanArgs& a, cudaStream_t stream, const char** why);
+wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const char** why);
+
+}  // namespace wkv

@@ -1,0 +1,346 @@
+"""Thin Python binding over the state-space operators of libwkv_b200.so
+(include/wkv_ssm.h): the short causal convolution, the per-head norm with
+position rotation and the selective scan.
+
+Like ``wkv``, argument marshalling only: every function checks tensor dtypes,
+shapes, devices and contiguity, allocates outputs and workspaces with torch
+and calls the C entry point of the same name on the tensors' device and its
+current stream.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import wkv as _wkv
+from .wkv import WkvError, _check, _dtype_code, _want, device_error  # noqa: F401  (WkvError, device_error: re-exported)
+
+SCAN_CKPT_LEN = 16  # WKV_SCAN_CKPT_LEN
+
+_i64, _int, _vp, _sz, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+# Every symbol include/wkv_ssm.h declares, with its ctypes signature.
+SIGNATURES = {
+    "wkv_conv_forward": (_int, [_i64, _i64, _i64, _int, _i64, _int] + [_vp] * 6),
+    "wkv_conv_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _i64]),
+    "wkv_conv_backward": (_int, [_i64, _i64, _i64, _int, _i64, _int] + [_vp] * 10 + [_sz, _vp]),
+    "wkv_conv_chunk_step": (_int, [_i64, _i64, _int, _i64, _int] + [_vp] * 4 + [_i64, _vp, _vp, _vp]),
+    "wkv_conv_decode_step": (_int, [_i64, _i64, _int, _i64, _int] + [_vp] * 6),
+    "wkv_norm_rotate": (_int, [_i64] * 6 + [_int] + [_vp] * 4 + [_f32, _vp, _vp, _i64, _int] + [_vp] * 3),
+    "wkv_norm_rotate_backward_workspace_bytes": (_sz, [_i64] * 5),
+    "wkv_norm_rotate_backward": (_int, [_i64] * 6 + [_int] + [_vp] * 6 + [_f32, _vp, _vp, _i64, _int] + [_vp] * 5 +
+                                 [_sz, _vp]),
+    "wkv_scan_forward": (_int, [_i64] * 5 + [_int] + [_vp] * 8 + [_int] + [_vp] * 5 + [_sz, _vp]),
+    "wkv_scan_forward_workspace_bytes": (_sz, [_i64] * 5),
+    "wkv_scan_ckpt_floats": (_sz, [_i64] * 4),
+    "wkv_scan_backward_workspace_bytes": (_sz, [_i64] * 5 + [_int]),
+    "wkv_scan_backward": (_int, [_i64] * 5 + [_int] + [_vp] * 8 + [_int] + [_vp] * 14 + [_sz, _vp]),
+    "wkv_scan_chunk_step": (_int, [_i64] * 4 + [_int] + [_vp] * 8 + [_int, _vp, _i64, _vp, _vp, _vp]),
+    "wkv_scan_decode_step": (_int, [_i64] * 4 + [_int] + [_vp] * 8 + [_int, _vp, _vp, _vp]),
+}
+
+_lib = _wkv.lib()
+for _name, (_res, _args) in SIGNATURES.items():
+    getattr(_lib, _name).restype = _res
+    getattr(_lib, _name).argtypes = _args
+
+
+def _call(name: str, dev: torch.device, *args):
+    """Calls the C entry point with the stream appended, with `dev` current."""
+    fn = getattr(_lib, name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+
+
+def _has(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
+    """The tensor's address, once it is known to be what the call reads or writes."""
+    if not (t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _want(t, name, dtype=dtype, shape=shape, device=dev)
+    return t.data_ptr()
+
+
+def _may(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
+    return None if t is None else _has(t, name, dtype, shape, dev)
+
+
+def _first(t: torch.Tensor, name: str, dims: int) -> torch.device:
+    """Checks the tensor that the sizes are taken from."""
+    _want(t, name)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    _dtype_code(t)
+    return t.device
+
+
+def _space(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
+    """(address, bytes, the tensor) of a workspace of at least `nbytes`."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _want(workspace, "workspace", device=dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+# ----------------------------------------------------------------------------
+# short causal convolution
+# ----------------------------------------------------------------------------
+
+def _taps(weight: torch.Tensor, C: int) -> int:
+    if weight.dim() != 2:
+        raise ValueError("weight must be [W, C]")
+    return weight.shape[0]
+
+
+def wkv_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     x_prev: Optional[torch.Tensor] = None, *, silu: bool = True,
+                     y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Depthwise causal convolution over the last W tokens. x: [B, T, C];
+    weight: [W, C] float32 (W 2..4, the last row meets the current token);
+    bias: [C] float32; x_prev: [B, W-1, C], the tokens before x (None: zeros).
+    Returns y like x, put through silu unless ``silu`` is false."""
+    dev = _first(x, "x", 3)
+    B, T, C = x.shape
+    W, f32 = _taps(weight, C), torch.float32
+    y = torch.empty_like(x) if y is None else y
+    _call("wkv_conv_forward", dev, B, T, C, _dtype_code(x), W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
+          _may(x_prev, "x_prev", x.dtype, (B, W - 1, C), dev), _has(y, "y", x.dtype, x.shape, dev))
+    return y
+
+
+def wkv_conv_backward(x, weight, gy, bias=None, x_prev=None, *, silu: bool = True, want_gx_prev: bool = False,
+                      gx=None, gweight=None, gbias=None, gx_prev=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of sum(gy * wkv_conv_forward(x, weight, bias, x_prev)).
+    Returns (gx, gweight, gbias, gx_prev); gbias is None without a bias,
+    gx_prev unless wanted (or a buffer is passed)."""
+    dev = _first(x, "x", 3)
+    B, T, C = x.shape
+    W, f32 = _taps(weight, C), torch.float32
+    gx = torch.empty_like(x) if gx is None else gx
+    gweight = torch.empty((W, C), dtype=f32, device=dev) if gweight is None else gweight
+    if gbias is None and bias is not None:
+        gbias = torch.empty(C, dtype=f32, device=dev)
+    if gx_prev is None and want_gx_prev:
+        gx_prev = torch.empty((B, W - 1, C), dtype=x.dtype, device=dev)
+    code = _dtype_code(x)
+    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_conv_backward_workspace_bytes(B, T, C, code, W)), dev)
+    _call("wkv_conv_backward", dev, B, T, C, code, W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
+          _may(x_prev, "x_prev", x.dtype, (B, W - 1, C), dev), _has(gy, "gy", x.dtype, x.shape, dev),
+          _has(gx, "gx", x.dtype, x.shape, dev), _has(gweight, "gweight", f32, (W, C), dev),
+          _may(gbias, "gbias", f32, (C,), dev), _may(gx_prev, "gx_prev", x.dtype, (B, W - 1, C), dev), ptr, nbytes)
+    return gx, gweight, gbias, gx_prev
+
+
+def wkv_conv_chunk_step(x, weight, cu_tokens: torch.Tensor, state: torch.Tensor, bias=None, *, silu: bool = True,
+                        y=None) -> torch.Tensor:
+    """The convolution over slots. x: [n, C], the tokens of all slots packed;
+    cu_tokens: int32 [S+1] on the device; state: [S, W-1, C] like x, the last
+    tokens of each slot, read and written in place. Returns y like x."""
+    dev = _first(x, "x", 2)
+    n, C = x.shape
+    W, S, f32 = _taps(weight, C), state.shape[0], torch.float32
+    y = torch.empty_like(x) if y is None else y
+    _call("wkv_conv_chunk_step", dev, S, C, _dtype_code(x), W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
+          _has(y, "y", x.dtype, x.shape, dev), n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
+          _has(state, "state", x.dtype, (S, W - 1, C), dev))
+    return y
+
+
+def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: bool = True, y=None) -> torch.Tensor:
+    """One token for every slot: x, y [S, C]; state as for wkv_conv_chunk_step."""
+    dev = _first(x, "x", 2)
+    S, C = x.shape
+    W, f32 = _taps(weight, C), torch.float32
+    y = torch.empty_like(x) if y is None else y
+    _call("wkv_conv_decode_step", dev, S, C, _dtype_code(x), W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
+          _has(y, "y", x.dtype, x.shape, dev), _has(state, "state", x.dtype, (S, W - 1, C), dev))
+    return y
+
+
+# ----------------------------------------------------------------------------
+# per-head norm with position rotation
+# ----------------------------------------------------------------------------
+
+def _heads(q, k, head_size):
+    """(device, dtype, B, T, Hq, Hk) of the queries and keys, either of which may be None."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q and k are both None")
+    dev = _first(lead, "q" if q is not None else "k", 3)
+    B, T, _ = lead.shape
+    heads = []
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            heads.append(0)
+            continue
+        if t.dim() != 3 or t.shape[2] % head_size:
+            raise ValueError(f"{name} must be [B, T, H * {head_size}], got {tuple(t.shape)}")
+        _has(t, name, lead.dtype, (B, T, t.shape[2]), dev)
+        heads.append(t.shape[2] // head_size)
+    return dev, lead.dtype, B, T, heads[0], heads[1]
+
+
+def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, K, dev):
+    f32 = torch.float32
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return R, (_may(q_weight, "q_weight", f32, (K,), dev), _may(k_weight, "k_weight", f32, (K,), dev),
+               _may(inv_freq, "inv_freq", f32, (R // 2,), dev),
+               _may(positions, "positions", torch.int32, (B, T), dev))
+
+
+def wkv_norm_rotate(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, head_size: int,
+                    eps: float = 1e-6, pos_offset: int = 0, interleaved: bool = False, q_out=None, k_out=None):
+    """Root-mean-square norm of every head of q and k and rotation of its first
+    2 * len(inv_freq) entries by position, in one pass. q: [B, T, Hq*K], k:
+    [B, T, Hk*K] (either may be None); q_weight, k_weight: [K] float32;
+    inv_freq: [R/2] float32 (None: no rotation); positions: int32 [B, T] (None:
+    pos_offset + t). q_out=q and k_out=k work in place. Returns (q_out, k_out)."""
+    dev, dtype, B, T, Hq, Hk = _heads(q, k, head_size)
+    R, (wq, wk, fr, po) = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, head_size, dev)
+    outs = []
+    for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+        o = torch.empty_like(t) if t is not None and o is None else o
+        if t is not None:
+            _has(o, name, dtype, t.shape, dev)
+        outs.append(o if t is not None else None)
+    p = [None if t is None else t.data_ptr() for t in (q, k, outs[0], outs[1])]
+    _call("wkv_norm_rotate", dev, B, T, Hq, Hk, head_size, R, _dtype_code(q if q is not None else k), p[0], p[1], wq, wk,
+          eps, fr, po, pos_offset, int(interleaved), p[2], p[3])
+    return outs[0], outs[1]
+
+
+def wkv_norm_rotate_backward(q, k, gq_out, gk_out, q_weight=None, k_weight=None, inv_freq=None, positions=None, *,
+                             head_size: int, eps: float = 1e-6, pos_offset: int = 0, interleaved: bool = False,
+                             gq=None, gk=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of sum(gq_out * q_out) + sum(gk_out * k_out) for wkv_norm_rotate
+    with the same arguments. Returns (gq, gk, gq_weight, gk_weight); a weight's
+    gradient is None where there is no such weight."""
+    dev, dtype, B, T, Hq, Hk = _heads(q, k, head_size)
+    K = head_size
+    R, (wq, wk, fr, po) = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, K, dev)
+    grads, weights = [], []
+    for name, t, go, g, w in (("q", q, gq_out, gq, q_weight), ("k", k, gk_out, gk, k_weight)):
+        if t is not None:
+            g = torch.empty_like(t) if g is None else g
+            _has(go, f"g{name}_out", dtype, t.shape, dev)
+            _has(g, f"g{name}", dtype, t.shape, dev)
+        grads.append(g if t is not None else None)
+        weights.append(None if w is None else torch.empty(K, dtype=torch.float32, device=dev))
+    p = [None if t is None else t.data_ptr() for t in
+         (q, k, gq_out if q is not None else None, gk_out if k is not None else None, *grads, *weights)]
+    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, K)), dev)
+    _call("wkv_norm_rotate_backward", dev, B, T, Hq, Hk, K, R, _dtype_code(q if q is not None else k), *p[:4], wq, wk,
+          eps, fr, po, pos_offset, int(interleaved), *p[4:], ptr, nbytes)
+    return (*grads, *weights)
+
+
+# ----------------------------------------------------------------------------
+# selective scan
+# ----------------------------------------------------------------------------
+
+def scan_ckpt_shape(B: int, T: int, C: int, N: int):
+    return (B, (T + SCAN_CKPT_LEN - 1) // SCAN_CKPT_LEN, C, N)
+
+
+def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dims):
+    """(device, sizes, addresses of the operands) of a scan over x of `dims` dimensions."""
+    dev = _first(x, "x", dims)
+    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    if A.dim() != 2 or A.shape[0] != C:
+        raise ValueError(f"A must be [C, N] with C = {C}, got {tuple(A.shape)}")
+    N, f32, e = A.shape[1], torch.float32, x.dtype
+    if Bm.dim() != dims or N == 0 or Bm.shape[-1] % N:
+        raise ValueError(f"Bm must be [..., G * N] with N = {N}, got {tuple(Bm.shape)}")
+    G, bc = Bm.shape[-1] // N, (*lead, Bm.shape[-1])
+    return dev, lead, C, N, G, (
+        x.data_ptr(), _has(dt, "dt", e, x.shape, dev), _has(A, "A", f32, (C, N), dev), _has(Bm, "Bm", e, bc, dev),
+        _has(Cm, "Cm", e, bc, dev), _may(D, "D", f32, (C,), dev), _may(z, "z", e, x.shape, dev),
+        _may(dt_bias, "dt_bias", f32, (C,), dev))
+
+
+def wkv_scan_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state=None, *, dt_softplus: bool = True,
+                     want_final_state: bool = True, want_ckpt: bool = False, y=None, final_state=None, ckpt=None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Selective scan. x, dt, z: [B, T, C]; A: [C, N] float32; Bm, Cm: [B, T,
+    G*N]; D, dt_bias: [C] float32; init_state: [B, C, N] float32.
+    Returns (y, final_state or None), or (y, final_state or None, ckpt) when
+    ``want_ckpt`` (or a ckpt buffer is passed)."""
+    dev, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    f32 = torch.float32
+    y = torch.empty_like(x) if y is None else y
+    if final_state is None and want_final_state:
+        final_state = torch.empty((B, C, N), dtype=f32, device=dev)
+    if ckpt is None and want_ckpt:
+        ckpt = torch.empty(scan_ckpt_shape(B, T, C, N), dtype=f32, device=dev)
+    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_scan_forward_workspace_bytes(B, T, C, N, G)), dev)
+    _call("wkv_scan_forward", dev, B, T, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
+          _may(init_state, "init_state", f32, (B, C, N), dev), _has(y, "y", x.dtype, x.shape, dev),
+          _may(final_state, "final_state", f32, (B, C, N), dev),
+          _may(ckpt, "ckpt", f32, scan_ckpt_shape(B, T, C, N), dev), ptr, nbytes)
+    return (y, final_state) if ckpt is None else (y, final_state, ckpt)
+
+
+def wkv_scan_backward(x, dt, A, Bm, Cm, gy, D=None, z=None, dt_bias=None, init_state=None, g_final=None, ckpt=None, *,
+                      dt_softplus: bool = True, want_g_init: bool = False, gx=None, gdt=None, gz=None,
+                      workspace: Optional[torch.Tensor] = None):
+    """Gradients of sum(gy * y) + sum(g_final * final_state) for
+    wkv_scan_forward with the same arguments. ckpt: the checkpoints it wrote
+    (None: regenerated). Returns (gx, gdt, gA, gB, gC, gD, gz, gdt_bias,
+    g_init); the gradient of an operand that is None is None, and so is g_init
+    unless wanted."""
+    dev, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    f32, e = torch.float32, x.dtype
+    gx = torch.empty_like(x) if gx is None else gx
+    gdt = torch.empty_like(x) if gdt is None else gdt
+    if z is None:
+        gz = None
+    elif gz is None:
+        gz = torch.empty_like(x)
+    gA, gB, gC = torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(Cm)
+    gD = None if D is None else torch.empty_like(D)
+    gbias = None if dt_bias is None else torch.empty_like(dt_bias)
+    g_init = torch.empty((B, C, N), dtype=f32, device=dev) if want_g_init else None
+    need = int(_lib.wkv_scan_backward_workspace_bytes(B, T, C, N, G, int(ckpt is not None)))
+    ptr, nbytes, workspace = _space(workspace, need, dev)
+    _call("wkv_scan_backward", dev, B, T, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
+          _may(init_state, "init_state", f32, (B, C, N), dev), _has(gy, "gy", e, x.shape, dev),
+          _may(g_final, "g_final", f32, (B, C, N), dev), _may(ckpt, "ckpt", f32, scan_ckpt_shape(B, T, C, N), dev),
+          _has(gx, "gx", e, x.shape, dev), _has(gdt, "gdt", e, x.shape, dev), gA.data_ptr(), gB.data_ptr(), gC.data_ptr(),
+          None if gD is None else gD.data_ptr(), _may(gz, "gz", e, x.shape, dev),
+          None if gbias is None else gbias.data_ptr(), None if g_init is None else g_init.data_ptr(), ptr, nbytes)
+    return gx, gdt, gA, gB, gC, gD, gz, gbias, g_init
+
+
+def wkv_scan_chunk_step(x, dt, A, Bm, Cm, cu_tokens: torch.Tensor, state: torch.Tensor, D=None, z=None, dt_bias=None,
+                        *, dt_softplus: bool = True, y=None) -> torch.Tensor:
+    """The scan over slots. x, dt, z: [n, C], Bm, Cm: [n, G*N], the tokens of all
+    slots packed; cu_tokens: int32 [S+1] on the device; state: [S, C, N]
+    float32, read and written in place. Returns y like x."""
+    dev, (n,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    S = state.shape[0]
+    y = torch.empty_like(x) if y is None else y
+    _call("wkv_scan_chunk_step", dev, S, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
+          _has(y, "y", x.dtype, x.shape, dev), n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
+          _has(state, "state", torch.float32, (S, C, N), dev))
+    return y
+
+
+def wkv_scan_decode_step(x, dt, A, Bm, Cm, state: torch.Tensor, D=None, z=None, dt_bias=None, *,
+                         dt_softplus: bool = True, y=None) -> torch.Tensor:
+    """One token for every slot: x, dt, z, y [S, C], Bm, Cm [S, G*N]; state as for
+    wkv_scan_chunk_step."""
+    dev, (S,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    y = torch.empty_like(x) if y is None else y
+    _call("wkv_scan_decode_step", dev, S, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
+          _has(y, "y", x.dtype, x.shape, dev), _has(state, "state", torch.float32, (S, C, N), dev))
+    return y
