@@ -91,22 +91,21 @@ __device__ __forceinline__ void ld_param(const float* p, float (&f)[N], float ot
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid_f(float x) { return rcp(__fadd_rn(1.f, ex2(__fmul_rn(x, -kLog2e)))); }
 
-// softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| <= 1, and its
-// derivative sigmoid(x). log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
-// the series of atanh (the first term left out is below 1.5e-8 of the sum):
-// it keeps its relative precision where e is small, which log(1 + e) loses.
-__device__ __forceinline__ float softplus_f(float x) {
-  const float e = ex2(__fmul_rn(fabsf(x), -kLog2e));
-  const float s = __fmul_rn(e, rcp(__fadd_rn(2.f, e)));
-  const float q = __fmul_rn(s, s);
-  float p = 1.f / 13.f;
-  p = __fmaf_rn(p, q, 1.f / 11.f);
-  p = __fmaf_rn(p, q, 1.f / 9.f);
-  p = __fmaf_rn(p, q, 1.f / 7.f);
-  p = __fmaf_rn(p, q, 1.f / 5.f);
-  p = __fmaf_rn(p, q, 1.f / 3.f);
-  p = __fmaf_rn(p, q, 1.f);
-  return __fmaf_rn(__fadd_rn(s, s), p, fmaxf(x, 0.f));
+// softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| <= 1, of a
+// pair. log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the series of atanh
+// (the first term left out is below 1.5e-8 of the sum): it keeps its relative
+// precision where e is small, which log(1 + e) loses.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+  const float2 e = make_float2(ex2(__fmul_rn(fabsf(x.x), -kLog2e)), ex2(__fmul_rn(fabsf(x.y), -kLog2e)));
+  const float2 s = mul2(e, rcp2(add2(e, splat2(2.f))));
+  const float2 q = mul2(s, s);
+  float2 p = fma2(splat2(1.f / 13.f), q, splat2(1.f / 11.f));
+  p = fma2(p, q, splat2(1.f / 9.f));
+  p = fma2(p, q, splat2(1.f / 7.f));
+  p = fma2(p, q, splat2(1.f / 5.f));
+  p = fma2(p, q, splat2(1.f / 3.f));
+  p = fma2(p, q, splat2(1.f));
+  return fma2(add2(s, s), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
 // Sums of NV values over the NL lanes that differ in the lane bits

@@ -106,13 +106,13 @@ struct ScanBwdArgs {
   float* part_a;   // [B*nseg][C][N]
   float* part_d;   // [2][B*nseg][C]: gD, gdt_bias
 };
-// Lanes that share a channel (4 states each): 2, 4, 8 or 16.
-inline int scan_lanes(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-// Channels per CTA.
-inline int scan_block_channels(int64_t N) { return std::min(64, 256 / scan_lanes(N)); }
+// State sizes the kernels are built for.
+inline int scan_padded_states(int64_t N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+// Channels per CTA, by the padded state size.
+constexpr int scan_cta_channels(int states) { return states <= 8 ? 64 : states <= 32 ? 32 : 16; }
 // CTAs that cover one group's channels.
 inline int64_t scan_group_blocks(int64_t C, int64_t N, int64_t G) {
-  return ceil_div(C / std::max<int64_t>(G, 1), scan_block_channels(N));
+  return ceil_div(C / std::max<int64_t>(G, 1), scan_cta_channels(scan_padded_states(N)));
 }
 // Pieces along T (1: uncut) of the forward and of the backward; each but the
 // last has seg_tiles * WKV_SCAN_CKPT_LEN tokens.

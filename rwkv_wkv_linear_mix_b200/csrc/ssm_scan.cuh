@@ -1,11 +1,18 @@
 // ssm_scan.cuh -- what the kernels of the selective scan share: the launch
 // geometry, where a CTA works, and the loads of a tile of tokens.
 //
-// A thread carries 4 states of each of 2 adjacent channels; LPC = 2, 4, 8 or
-// 16 lanes side by side share the pair, so that 4 LPC >= N. The states above
-// N are zero and stay zero (their B is zero). A CTA covers CB channels of one
-// group, so that B and C are one row of numbers per token for all of them,
-// and walks its tokens in tiles of 16.
+// A thread carries S = 2 or 4 states of each of 2 adjacent channels; LPC lanes
+// side by side share the pair, so that S LPC >= N. The states above N are zero
+// and stay zero (their B is zero). A CTA covers CB channels of one group, so
+// that B and C are one row of numbers per token for all of them, and walks its
+// tokens in tiles of 16.
+//
+// Packed pairs hold one state of both channels. Sums over lanes are taken in
+// halving steps, and a lane's order of channels and states is chosen so that
+// the first steps need no selects: lane bit 0 swaps the two channels, so that
+// the second one's sums are always the ones to give away, and (backward) the
+// bits above the lane group permute the states likewise. B and C, d and the
+// rest lie in shared memory in each order.
 #pragma once
 
 #include "ssm_device.cuh"
@@ -14,16 +21,20 @@ namespace wkv {
 
 constexpr int kScanTile = WKV_SCAN_CKPT_LEN;  // tokens per tile
 
-template <class E, int LPC>
+// S: states per thread.
+template <class E, int LPC_, int S_>
 struct ScanGeom {
-  static constexpr int NP = 4 * LPC;                        // padded states
-  static constexpr int CB = LPC <= 4 ? 64 : 256 / LPC;      // channels per CTA
-  static constexpr int THREADS = CB / 2 * LPC;
-  static constexpr int VN = 16 / (int)sizeof(E);            // channels per 16-byte load
-  static constexpr int VPR = CB / VN;                       // such loads per token
-  static constexpr int PT = (kScanTile * VPR + THREADS - 1) / THREADS;  // per thread and tile
-  static constexpr int PB = (kScanTile * LPC + THREADS - 1) / THREADS;  // 4-state loads of B or C
-  static_assert(THREADS % VPR == 0, "a thread's loads keep their channels");
+  static constexpr int LPC = LPC_, S = S_;
+  static constexpr int NP = S * LPC;                  // padded states
+  static constexpr int CB = scan_cta_channels(NP);   // channels per CTA
+  static constexpr int HB = CB / 2;                   // channel pairs per CTA
+  static constexpr int THREADS = HB * LPC;
+  static constexpr int PT = kScanTile * HB / THREADS; // channel pairs a thread converts per tile
+  static constexpr int ROWS = THREADS / HB;           // tokens apart
+  static constexpr int VN = 16 / (int)sizeof(E);      // channels per 16-byte copy
+  static constexpr int VPR = CB / VN;                 // such copies per token
+  static constexpr int BPR = NP / 4;                  // 4-state copies of B or C per token
+  static_assert(THREADS % 32 == 0 && kScanTile % ROWS == 0, "whole rows");
 };
 
 struct ScanParams {
@@ -65,93 +76,215 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanParams& p) {
   return w;
 }
 
-// The loads of one tile of an activation [tokens][C]: vector i of a thread is
-// channels c0 + (tid % VPR) * VN .. of token (tid + i THREADS) / VPR.
-template <class E, int LPC>
-struct ScanRows {
-  using Geo = ScanGeom<E, LPC>;
-  Pack<E, Geo::VN> v[Geo::PT];
-  // base: token 0 of the sequence; tokens t0 .. tend-1 exist
-  __device__ __forceinline__ void load(const E* base, int64_t t0, int64_t tend, int64_t C, int64_t c0, int64_t cend) {
-    const int col = (int)threadIdx.x % Geo::VPR * Geo::VN;
-#pragma unroll
-    for (int i = 0; i < Geo::PT; ++i) {
-      const int t = ((int)threadIdx.x + i * Geo::THREADS) / Geo::VPR;
-      v[i].zero();
-      if (t < kScanTile && t0 + t < tend && c0 + col < cend) v[i].load(base + (t0 + t) * C + c0 + col);
-    }
-  }
-};
+// One copy of 8 or 16 bytes to shared memory that the thread does not wait
+// for; zeros where there is nothing to copy (src is then not read).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
+  static_assert(BYTES == 8 || BYTES == 16, "copy sizes");
+  const int n = there ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// The loads of one tile of B or C, [tokens][G N], and their way into a
-// [16][NP] float32 table in shared memory.
-template <class E, int LPC>
-struct ScanVecs {
-  using Geo = ScanGeom<E, LPC>;
-  Pack<E, 4> v[Geo::PB];
-  __device__ __forceinline__ void load(const E* base, int64_t t0, int64_t tend, int64_t GN, int64_t gN, int64_t N) {
+// A tile of tokens as stored: NT activations, B and C, with zeros past the
+// sequence, the group's channels and the N states.
+template <class E, class Geo, int NT>
+struct ScanRaw {
+  E act[NT][kScanTile][Geo::CB];
+  E bc[2][kScanTile][Geo::NP];
+
+  // at: token t0 of the sequence times C, plus c0; left: tokens from t0 to the end
+  __device__ __forceinline__ void load_act(int which, const E* base, int64_t at, int64_t C, int left, int channels) {
 #pragma unroll
-    for (int i = 0; i < Geo::PB; ++i) {
-      const int k = (int)threadIdx.x + i * Geo::THREADS;
-      const int t = k / LPC, n = k % LPC * 4;
-      v[i].zero();
-      if (t < kScanTile && t0 + t < tend && n < N) v[i].load(base + (t0 + t) * GN + gN + n);
+    for (int i = 0; i < (kScanTile * Geo::VPR + Geo::THREADS - 1) / Geo::THREADS; ++i) {
+      const int k = (int)threadIdx.x + i * Geo::THREADS, t = k / Geo::VPR, col = k % Geo::VPR * Geo::VN;
+      if (t < kScanTile) {
+        const bool there = t < left && col < channels;
+        copy_async<16>(&act[which][t][col], there ? base + at + t * C + col : base, there);
+      }
     }
   }
-  __device__ __forceinline__ void put(float* table) const {
+  // at: token t0 times G N, plus the group's first state
+  __device__ __forceinline__ void load_bc(int which, const E* base, int64_t at, int64_t GN, int left, int N) {
 #pragma unroll
-    for (int i = 0; i < Geo::PB; ++i) {
+    for (int i = 0; i < (kScanTile * Geo::BPR + Geo::THREADS - 1) / Geo::THREADS; ++i) {
+      const int k = (int)threadIdx.x + i * Geo::THREADS, t = k / Geo::BPR, n = k % Geo::BPR * 4;
+      if (t < kScanTile) {
+        const bool there = t < left && n < N;
+        copy_async<4 * (int)sizeof(E)>(&bc[which][t][n], there ? base + at + t * GN + n : base, there);
+      }
+    }
+  }
+  // B or C into float32 rows [16][V][NP], row m of a token with state n at n ^ m
+  template <int V>
+  __device__ __forceinline__ void put_bc(int which, float* table) const {
+#pragma unroll
+    for (int i = 0; i < (kScanTile * Geo::BPR + Geo::THREADS - 1) / Geo::THREADS; ++i) {
       const int k = (int)threadIdx.x + i * Geo::THREADS;
-      if (k / LPC < kScanTile) {
+      if (k < kScanTile * Geo::BPR) {
+        Pack<E, 4> v;
+        v.load(&bc[which][0][0] + 4 * k);
         float f[4];
-        v[i].get(f);
-        *reinterpret_cast<float4*>(table + k * 4) = make_float4(f[0], f[1], f[2], f[3]);
+        v.get(f);
+#pragma unroll
+        for (int m = 0; m < V; ++m)
+          *reinterpret_cast<float4*>(table + (k / Geo::BPR * V + m) * Geo::NP + k % Geo::BPR * 4) =
+              make_float4(f[m], f[1 ^ m], f[2 ^ m], f[3 ^ m]);
       }
     }
   }
 };
 
-// Four states as two packed pairs.
-struct State4 {
-  float2 q[2];
+// S states of a pair of channels: n[j] holds a state of the lane's first and
+// second channel. (Storing numbers twice in shared memory to spare the moves
+// that double them does not pay: a load costs a cycle per register it fills,
+// whatever the lanes share.)
+template <int S>
+struct States {
+  float2 n[S];
 };
-__device__ __forceinline__ State4 ld_state(const float* p, bool there) {
-  State4 s = {{splat2(0.f), splat2(0.f)}};
-  if (there) {
+// A row of S numbers of a table, each for both channels.
+template <int S>
+struct Row {
+  float n[S];
+};
+template <int S>
+__device__ __forceinline__ Row<S> ld_row(const float* p) {
+  Row<S> r;
+  if constexpr (S == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    r.n[0] = f.x, r.n[1] = f.y;
+  } else {
     const float4 f = *reinterpret_cast<const float4*>(p);
-    s.q[0] = make_float2(f.x, f.y);
-    s.q[1] = make_float2(f.z, f.w);
+    r.n[0] = f.x, r.n[1] = f.y, r.n[2] = f.z, r.n[3] = f.w;
   }
-  return s;
+  return r;
 }
-__device__ __forceinline__ void st_state(float* p, const State4& s) {
-  *reinterpret_cast<float4*>(p) = make_float4(s.q[0].x, s.q[0].y, s.q[1].x, s.q[1].y);
+// The order of a lane: its first channel is swap (0 or 1) of the pair, its
+// register j holds state j ^ perm of its S.
+struct LaneOrder {
+  int swap, perm;
+};
+// From / to [channel][N] rows; p: the lane's states of the pair's channel 0.
+template <int S>
+__device__ __forceinline__ States<S> ld_states(const float* p, int64_t N, bool there, LaneOrder o) {
+  States<S> r;
+  const float* a = p + (o.swap ? N : 0);
+  const float* b = p + (o.swap ? 0 : N);
+#pragma unroll
+  for (int j = 0; j < S; ++j) r.n[j] = there ? make_float2(a[j ^ o.perm], b[j ^ o.perm]) : splat2(0.f);
+  return r;
 }
-__device__ __forceinline__ State4 lds_state(const float* p) {
-  const float4 f = *reinterpret_cast<const float4*>(p);
-  return {{make_float2(f.x, f.y), make_float2(f.z, f.w)}};
+template <int S>
+__device__ __forceinline__ void st_states(float* p, int64_t N, const States<S>& s, LaneOrder o) {
+  float* a = p + (o.swap ? N : 0);
+  float* b = p + (o.swap ? 0 : N);
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    a[j ^ o.perm] = s.n[j].x;
+    b[j ^ o.perm] = s.n[j].y;
+  }
+}
+// The same for a lane in natural state order, as wide accesses.
+template <int S>
+__device__ __forceinline__ States<S> ld_states_wide(const float* p, int64_t N, bool there) {
+  States<S> r;
+  Row<S> a = {}, b = {};
+  if (there) {
+    a = ld_row<S>(p);
+    b = ld_row<S>(p + N);
+  }
+#pragma unroll
+  for (int j = 0; j < S; ++j) r.n[j] = make_float2(a.n[j], b.n[j]);
+  return r;
+}
+template <int S>
+__device__ __forceinline__ void st_states_wide(float* p, int64_t N, const States<S>& s, int swap) {
+  float* a = p + (swap ? N : 0);
+  float* b = p + (swap ? 0 : N);
+  if constexpr (S == 2) {
+    *reinterpret_cast<float2*>(a) = make_float2(s.n[0].x, s.n[1].x);
+    *reinterpret_cast<float2*>(b) = make_float2(s.n[0].y, s.n[1].y);
+  } else {
+    *reinterpret_cast<float4*>(a) = make_float4(s.n[0].x, s.n[1].x, s.n[2].x, s.n[3].x);
+    *reinterpret_cast<float4*>(b) = make_float4(s.n[0].y, s.n[1].y, s.n[2].y, s.n[3].y);
+  }
+}
+template <int S>
+__device__ __forceinline__ States<S> scale_states(const States<S>& s, float f) {
+  States<S> r;
+#pragma unroll
+  for (int j = 0; j < S; ++j) r.n[j] = mul2(s.n[j], splat2(f));
+  return r;
 }
 
-// d_t of a token from what is stored.
-__device__ __forceinline__ float scan_step_size(float dt, float bias, bool softplus) {
-  const float raw = __fadd_rn(dt, bias);
-  return softplus ? softplus_f(raw) : raw;
+// The step sizes d of a pair of channels from what is stored.
+__device__ __forceinline__ float2 scan_step_size2(float2 dt, float2 bias, bool softplus) {
+  const float2 raw = add2(dt, bias);
+  return softplus ? softplus2(raw) : raw;
 }
-// The decays of 4 states over step size d (A2 = A log2 e).
-__device__ __forceinline__ State4 scan_decay(float d, const State4& A2) {
-  return {{ex2_2(mul2(splat2(d), A2.q[0])), ex2_2(mul2(splat2(d), A2.q[1]))}};
+// The decays of the states over step sizes d (A2 = A log2 e). ex2.approx was
+// measured 2e-8 low on average over [-1, 0] (against float64, 2^20 points a
+// decade), which a state that remembers a thousand tokens adds up to 2e-5;
+// the exponent's multiply-add makes up for it at no cost.
+constexpr float kEx2Low = 3.0e-8f;
+template <int S>
+__device__ __forceinline__ States<S> scan_decay(float2 d, const States<S>& A2) {
+  States<S> r;
+#pragma unroll
+  for (int j = 0; j < S; ++j) r.n[j] = ex2_2(fma2(d, A2.n[j], splat2(kEx2Low)));
+  return r;
 }
-// h <- a h + dx B, and the lane's part of sum_n C h.
-__device__ __forceinline__ void scan_absorb(State4& h, const State4& a, float dx, const State4& Bv) {
-  h.q[0] = fma2(a.q[0], h.q[0], mul2(splat2(dx), Bv.q[0]));
-  h.q[1] = fma2(a.q[1], h.q[1], mul2(splat2(dx), Bv.q[1]));
+// h <- a h + dx B
+template <int S>
+__device__ __forceinline__ void scan_absorb(States<S>& h, const States<S>& a, float2 dx, const Row<S>& Bv) {
+#pragma unroll
+  for (int j = 0; j < S; ++j) h.n[j] = fma2(a.n[j], h.n[j], mul2(dx, splat2(Bv.n[j])));
 }
-__device__ __forceinline__ float scan_dot(const State4& a, const State4& b) {
-  const float2 s = fma2(a.q[1], b.q[1], mul2(a.q[0], b.q[0]));
-  return __fadd_rn(s.x, s.y);
+// The sums over the lane's states of a b, of both channels: each two states by
+// one multiply-add, then these in pairs, and on in the lane exchanges, so
+// that the sum does not depend on how many states a lane holds.
+template <int S>
+__device__ __forceinline__ float2 scan_dot(const States<S>& a, const States<S>& b) {
+  const float2 s = fma2(a.n[1], b.n[1], mul2(a.n[0], b.n[0]));
+  if constexpr (S == 4) return add2(s, fma2(a.n[3], b.n[3], mul2(a.n[2], b.n[2])));
+  return s;
 }
-__device__ __forceinline__ State4 scale4(const State4& s, float f) {
-  return {{mul2(s.q[0], splat2(f)), mul2(s.q[1], splat2(f))}};
+template <int S>
+__device__ __forceinline__ float2 scan_dot(const States<S>& a, const Row<S>& b) {
+  States<S> r;
+#pragma unroll
+  for (int j = 0; j < S; ++j) r.n[j] = splat2(b.n[j]);
+  return scan_dot<S>(a, r);
+}
+// h <- a h + s, the fold of a piece's end state.
+template <int S>
+__device__ __forceinline__ void scan_fold(States<S>& h, const States<S>& a, const States<S>& s) {
+#pragma unroll
+  for (int j = 0; j < S; ++j) h.n[j] = fma2(a.n[j], h.n[j], s.n[j]);
+}
+// One number per token of 4 tokens for each of the two channels, summed over
+// the LPC lanes of the pair: the lane ends with its first channel's sums of
+// tokens pair_sum_first<LPC>(g) .. , kPairSums<LPC> of them (16 lanes: the
+// upper 8 have copies).
+template <int LPC>
+constexpr int kPairSums = LPC >= 8 ? 1 : 8 / LPC;
+template <int LPC>
+__device__ __forceinline__ int pair_sum_first(int g) {
+  return reduce_scatter_first<4, LPC / 2>(g / 2);
+}
+template <int LPC>
+__device__ __forceinline__ void pair_sums(const float2 (&s)[4], float (&out)[kPairSums<LPC>], int lane) {
+  float v[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) v[t] = __fadd_rn(s[t].x, __shfl_xor_sync(0xffffffffu, s[t].y, 1));
+  reduce_scatter<4, LPC / 2, 2>(v, lane);
+#pragma unroll
+  for (int t = 0; t < kPairSums<LPC>; ++t) out[t] = v[t];
 }
 
 // Host: the parameters a launch has in common.

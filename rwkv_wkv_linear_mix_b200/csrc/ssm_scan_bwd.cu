@@ -7,9 +7,9 @@
 //     gz = gy s silu'(z)             gdt = gd softplus'(dt + bias)
 //
 // The states are recomputed from the forward's checkpoints, one per tile of
-// 16 tokens: a tile is walked in two halves of 8 tokens, whose decays a and
-// decayed states a h_{t-1} stay in registers between the recompute (which
-// also gives gC and s) and the reverse walk. a h is kept rather than formed
+// 16 tokens: a tile is walked in sub-blocks, whose decays a and decayed
+// states a h_{t-1} stay in registers between the recompute (which also gives
+// gC and s) and the reverse walk. a h is kept rather than formed
 // as h - d x B, which would cancel where the decay is strong. Sums over the
 // states of a channel and over the channels of a group are taken in halving
 // steps across lanes; a CTA's gB and gC leave as one partial row per token,
@@ -25,144 +25,186 @@ namespace wkv {
 
 namespace {
 
-template <int CB, int NP, int WARPS>
-struct BwdBuf {
-  float4 dd[kScanTile][CB / 2];  // per channel pair: d0, d0 x0, d1, d1 x1
-  float4 xg[kScanTile][CB / 2];  // x0, gs0, x1, gs1
-  float4 sz[kScanTile][CB / 2];  // softplus'(raw0), gy0 silu'(z0), ... of channel 1
-  float B[kScanTile][NP];
-  float C[kScanTile][NP];
-  float sum[2][WARPS][kScanTile][NP];  // gB, gC of each warp's channels
+enum { kActX, kActDt, kActGy, kActZ, kActs };
+
+// Tokens whose decays and decayed states are in registers at a time, and the
+// interval of the states that a tile's first walk leaves in shared memory.
+constexpr int kBwdSub = 4;
+
+template <class E, class Geo>
+struct ScanBwdShared {
+  static constexpr int WARPS = Geo::THREADS / 32;
+  ScanRaw<E, Geo, kActs> raw;                    // the tile that is next
+  // rows padded by a pair (32 bytes), since lanes that finish outputs read 4 tokens at once
+  float4 dd[kScanTile][Geo::HB + 1][2];          // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
+  float4 gx[kScanTile][Geo::HB + 1][2];          // gs0, gs1, x0, x1; and swapped
+  float2 sz[kScanTile][Geo::HB + 2][2];          // per channel: softplus'(raw), gy silu'(z)
+  float B[kScanTile][Geo::S][Geo::NP];           // in each order of a lane's states
+  float C[kScanTile][Geo::S][Geo::NP];
+  float sum[2][WARPS][kScanTile][Geo::NP];       // gB, gC of each warp's channels
+  // the states before token 0, SUB, 2 SUB, ... of the tile, per thread and channel
+  float h[kScanTile / kBwdSub][2][Geo::THREADS][Geo::S];
 };
 
-template <class E, int LPC, bool Z>
-__global__ void __launch_bounds__(ScanGeom<E, LPC>::THREADS) scan_bwd_kernel(const ScanParams p) {
-  using Geo = ScanGeom<E, LPC>;
-  constexpr int CB = Geo::CB, NP = Geo::NP, VN = Geo::VN;
-  constexpr int WARPS = Geo::THREADS / 32;
-  constexpr int HALF = kScanTile / 2;
-  constexpr int TG = LPC <= 8 ? 4 : 8;  // tokens whose channel outputs are summed together
-  constexpr int RL = 32 / LPC;          // lanes of a warp that share their states' index
-  using Buf = BwdBuf<CB, NP, WARPS>;
+// Sums over the lanes that hold the same states of other channel pairs (lane
+// bits LPC and up), for the S states of two tokens. The lane's state order
+// (perm) makes the first steps select-free; the step after them exchanges
+// tokens, further ones leave copies. GV results per lane: result v is state
+// S g + (v % GS) ^ perm of token `tok` (of both, v / GS, where every step was
+// one over states).
+template <int LPC, int S>
+struct ChannelSums {
+  static constexpr int RL = 32 / LPC;                          // lanes to add up
+  static constexpr int PS = RL < S ? RL : S;                   // of these, by the order of states
+  static constexpr int GS = S / PS;                            // states left then
+  static constexpr bool TOK = RL > PS;                         // whether a step exchanges the tokens
+  static constexpr int GV = TOK ? GS : 2 * GS;
+  __device__ static __forceinline__ int perm(int lane) {
+    // bit b above the lane group halves the states S/2, S/4, .. apart
+    int m = 0;
+#pragma unroll
+    for (int b = 0; (1 << b) < PS; ++b)
+      if (lane & (LPC << b)) m |= S >> (b + 1);
+    return m;
+  }
+  // v[t][j]: token t, register j
+  __device__ static __forceinline__ void sum(float (&v)[2][S], float (&out)[GV], int lane) {
+#pragma unroll
+    for (int b = 0; (1 << b) < PS; ++b) {
+      const int half = S >> (b + 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < half; ++j)
+          v[t][j] = __fadd_rn(v[t][j], __shfl_xor_sync(0xffffffffu, v[t][j + half], LPC << b));
+    }
+    if constexpr (TOK) {
+      static_assert(GS == 1, "tokens are exchanged once one state is left");
+      float r[2] = {v[0][0], v[1][0]};
+      reduce_scatter<2, RL / PS, LPC * PS>(r, lane);
+      out[0] = r[0];
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < GS; ++j) out[t * GS + j] = v[t][j];
+    }
+  }
+  __device__ static __forceinline__ int token(int v, int lane) { return TOK ? (lane / (LPC * PS)) & 1 : v / GS; }
+};
+
+template <class E, int LPC, int S, bool Z>
+__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) scan_bwd_kernel(const ScanParams p) {
+  using Geo = ScanGeom<E, LPC, S>;
+  using Shared = ScanBwdShared<E, Geo>;
+  constexpr int NP = Geo::NP, WARPS = Shared::WARPS, SUB = kBwdSub;
+  using Sums = ChannelSums<LPC, S>;
   extern __shared__ float4 smem4[];
-  Buf* buf = reinterpret_cast<Buf*>(smem4);
-  const ScanPlace w = scan_place<CB>(p);
+  Shared& sm = *reinterpret_cast<Shared*>(smem4);
+  const ScanPlace w = scan_place<Geo::CB>(p);
   const int tid = threadIdx.x;
   const int64_t T = p.T, first = w.b * T;
   const int64_t tbeg = w.seg * p.seg_tokens;
   const int64_t tend = w.seg == p.nseg - 1 ? T : tbeg + p.seg_tokens;
-  const E* xg = static_cast<const E*>(p.x) + first * p.C;
-  const E* dtg = static_cast<const E*>(p.dt) + first * p.C;
-  const E* gyg = static_cast<const E*>(p.gy) + first * p.C;
-  const E* zg = Z ? static_cast<const E*>(p.z) + first * p.C : nullptr;
-  E* gxg = static_cast<E*>(p.gx) + first * p.C;
-  E* gdtg = static_cast<E*>(p.gdt) + first * p.C;
-  E* gzg = Z ? static_cast<E*>(p.gz) + first * p.C : nullptr;
+  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
   const int64_t GN = p.G * p.N, gN = w.g * p.N;
-  const E* Bg = static_cast<const E*>(p.Bm) + first * GN;
-  const E* Cg = static_cast<const E*>(p.Cm) + first * GN;
+  const int channels = (int)(w.cend - w.c0);
+  auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
+  auto tokens = [&](int i) { return (int)min(tend - start(i), (int64_t)kScanTile); };
 
-  const int col = tid % Geo::VPR * VN;
-  const bool col_on = w.c0 + col < w.cend;
-  float bias[VN];
-  ld_param<VN>(p.dt_bias && col_on ? p.dt_bias + w.c0 + col : nullptr, bias, 0.f);
-
-  ScanRows<E, LPC> rx, rdt, rz, rgy;
-  ScanVecs<E, LPC> rb, rc;
-  auto load = [&](int64_t t0) {
-    rx.load(xg, t0, tend, p.C, w.c0, w.cend);
-    rdt.load(dtg, t0, tend, p.C, w.c0, w.cend);
-    rgy.load(gyg, t0, tend, p.C, w.c0, w.cend);
-    if constexpr (Z) rz.load(zg, t0, tend, p.C, w.c0, w.cend);
-    rb.load(Bg, t0, tend, GN, gN, p.N);
-    rc.load(Cg, t0, tend, GN, gN, p.N);
+  auto load = [&](int i) {
+    ScanRaw<E, Geo, kActs>& r = sm.raw;
+    const int left = tokens(i);
+    const int64_t at = (first + start(i)) * p.C + w.c0, bc = (first + start(i)) * GN + gN;
+    r.load_act(kActX, static_cast<const E*>(p.x), at, p.C, left, channels);
+    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
+    r.load_act(kActGy, static_cast<const E*>(p.gy), at, p.C, left, channels);
+    if constexpr (Z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
+    r.load_bc(0, static_cast<const E*>(p.Bm), bc, GN, left, (int)p.N);
+    r.load_bc(1, static_cast<const E*>(p.Cm), bc, GN, left, (int)p.N);
+    copy_async_commit();
   };
-  auto convert = [&](Buf& o, int64_t t0) {
-    rb.put(&o.B[0][0]);
-    rc.put(&o.C[0][0]);
+  const int lp = tid % Geo::HB;
+  const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);
+  auto convert = [&](int i) {
+    const ScanRaw<E, Geo, kActs>& r = sm.raw;
+    const int left = tokens(i);
+    r.template put_bc<S>(0, &sm.B[0][0][0]);
+    r.template put_bc<S>(1, &sm.C[0][0][0]);
 #pragma unroll
-    for (int i = 0; i < Geo::PT; ++i) {
-      const int t = (tid + i * Geo::THREADS) / Geo::VPR;
-      if (t < kScanTile) {
-        const bool real = t0 + t < tend;
-        float x[VN], dt[VN], z[VN], gy[VN];
-        rx.v[i].get(x);
-        rdt.v[i].get(dt);
-        rgy.v[i].get(gy);
-        if constexpr (Z) rz.v[i].get(z);
-#pragma unroll
-        for (int n = 0; n < VN; n += 2) {
-          float d[2], gs[2], sp[2], gz[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float raw = __fadd_rn(dt[n + k], bias[n + k]);
-            // a token past the end: d, x, gs and sp are 0, which passes Q on
-            // and leaves every sum alone
-            d[k] = !real ? 0.f : p.softplus ? softplus_f(raw) : raw;
-            sp[k] = !real ? 0.f : p.softplus ? sigmoid_f(raw) : 1.f;
-            gs[k] = gy[n + k];
-            gz[k] = 0.f;
-            if constexpr (Z) {
-              const float s = sigmoid_f(z[n + k]);
-              gs[k] = __fmul_rn(gy[n + k], __fmul_rn(z[n + k], s));
-              gz[k] = __fmul_rn(gy[n + k], __fmul_rn(s, __fmaf_rn(z[n + k], __fsub_rn(1.f, s), 1.f)));
-            }
-          }
-          o.dd[t][(col + n) / 2] = make_float4(d[0], __fmul_rn(d[0], x[n]), d[1], __fmul_rn(d[1], x[n + 1]));
-          o.xg[t][(col + n) / 2] = make_float4(x[n], gs[0], x[n + 1], gs[1]);
-          o.sz[t][(col + n) / 2] = make_float4(sp[0], gz[0], sp[1], gz[1]);
-        }
+    for (int j = 0; j < Geo::PT; ++j) {
+      const int t = tid / Geo::HB + j * Geo::ROWS;
+      const float2 raw = add2(ld_pair(&r.act[kActDt][t][2 * lp]), bias), x = ld_pair(&r.act[kActX][t][2 * lp]);
+      // a token past the end: d, x, gs and softplus' are 0, which passes Q on
+      // and leaves every sum alone
+      const bool real = t < left;
+      const float2 d = !real ? splat2(0.f) : p.softplus ? softplus2(raw) : raw;
+      const float2 sp = !real ? splat2(0.f) : p.softplus ? sigmoid2(raw) : splat2(1.f);
+      const float2 gy = ld_pair(&r.act[kActGy][t][2 * lp]);
+      float2 gs = gy, gz = splat2(0.f);
+      if constexpr (Z) {
+        const float2 z = ld_pair(&r.act[kActZ][t][2 * lp]), s = sigmoid2(z);
+        gs = mul2(gy, mul2(z, s));
+        gz = mul2(gy, mul2(s, fma2(z, sub2(splat2(1.f), s), splat2(1.f))));
       }
+      const float2 dx = mul2(d, x);
+      sm.dd[t][lp][0] = make_float4(d.x, d.y, dx.x, dx.y);
+      sm.dd[t][lp][1] = make_float4(d.y, d.x, dx.y, dx.x);
+      sm.gx[t][lp][0] = make_float4(gs.x, gs.y, x.x, x.y);
+      sm.gx[t][lp][1] = make_float4(gs.y, gs.x, x.y, x.x);
+      *reinterpret_cast<float4*>(sm.sz[t][lp]) = make_float4(sp.x, gz.x, sp.y, gz.y);
     }
   };
 
   const int pair = tid / LPC, g = tid % LPC, warp = tid / 32, lane = tid % 32;
+  const LaneOrder order{g & 1, Sums::perm(lane)};
   const int64_t c = w.c0 + 2 * pair;
-  const bool ch_on = c < w.cend, on = ch_on && 4 * g < p.N;
+  const bool ch_on = 2 * pair < channels, on = ch_on && S * g < p.N;
   const int64_t nck = (T + kScanTile - 1) / kScanTile;
-  State4 A2[2], gA[2], q[2];  // q: a_{t+1} Q_{t+1}
-  float D[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    A2[k] = scale4(ld_state(p.A + (c + k) * p.N + 4 * g, on), kLog2e);
-    gA[k].q[0] = gA[k].q[1] = splat2(0.f);
-    q[k] = ld_state(p.g_final + (w.b * p.C + c + k) * p.N + 4 * g, on && p.g_final);
-    D[k] = p.D && ch_on ? p.D[c + k] : 0.f;
-  }
+  const int64_t state_at = (w.b * p.C + c) * p.N + S * g;
+  const States<S> A2 = scale_states<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order), kLog2e);
+  States<S> gA = ld_states<S>(nullptr, 0, false, order);
+  States<S> q = ld_states<S>(p.g_final + state_at, p.N, on && p.g_final, order);  // a_{t+1} Q_{t+1}
+  const float D = p.D && ch_on ? p.D[c + order.swap] : 0.f;
   {
     const float* sums = p.carry + p.B * p.nseg * p.C * p.N;
     for (int j = p.nseg - 1; j > w.seg; --j) {
-      const int64_t row = (w.b * p.nseg + j) * p.C + c;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (on) {
-          const State4 s = ld_state(p.carry + (row + k) * p.N + 4 * g, true);
-          const State4 a = scan_decay(sums[row + k], A2[k]);
-          q[k].q[0] = fma2(a.q[0], q[k].q[0], s.q[0]);
-          q[k].q[1] = fma2(a.q[1], q[k].q[1], s.q[1]);
-        }
+      if (on) {
+        const int64_t row = (w.b * p.nseg + j) * p.C + c;
+        const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
+        scan_fold(q, scan_decay(make_float2(sums[row + order.swap], sums[row + 1 - order.swap]), A2), s);
       }
     }
   }
-  float gD[2] = {0.f, 0.f}, gdb[2] = {0.f, 0.f};
+  float gD = 0.f, gdb = 0.f;  // of the lane's first channel
 
-  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
-  auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
-  auto ld_ckpt = [&](int i, State4 (&h)[2]) {
-    const int64_t m = start(i) / kScanTile;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) h[k] = ld_state(p.ckpt + ((w.b * nck + m) * p.C + c + k) * p.N + 4 * g, on);
+  auto ld_ckpt = [&](int i) {
+    return ld_states<S>(p.ckpt + ((w.b * nck + start(i) / kScanTile) * p.C + c) * p.N + S * g, p.N, on, order);
   };
-  auto put_sums = [&](const Buf& o, int64_t t0) {
+  auto st_h = [&](int i, const States<S>& h) {
+    float a[S], b[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) a[j] = h.n[j].x, b[j] = h.n[j].y;
+    if constexpr (S == 2) {
+      *reinterpret_cast<float2*>(sm.h[i][0][tid]) = make_float2(a[0], a[1]);
+      *reinterpret_cast<float2*>(sm.h[i][1][tid]) = make_float2(b[0], b[1]);
+    } else {
+      *reinterpret_cast<float4*>(sm.h[i][0][tid]) = make_float4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<float4*>(sm.h[i][1][tid]) = make_float4(b[0], b[1], b[2], b[3]);
+    }
+  };
+  auto put_sums = [&](int i) {
     // the tile's gB, gC of this CTA's channels
-    constexpr int PER = 2 * kScanTile * LPC;
-    for (int i = tid; i < PER; i += Geo::THREADS) {
-      const int n = i % LPC * 4, t = i / LPC % kScanTile, which = i / (LPC * kScanTile);
-      if (t0 + t < tend && n < p.N) {
-        float4 s = *reinterpret_cast<const float4*>(&o.sum[which][0][t][n]);
+    const int left = tokens(i);
+    const int64_t t0 = start(i);
+    constexpr int VPR = NP / 4;
+    for (int k = tid; k < 2 * kScanTile * VPR; k += Geo::THREADS) {
+      const int n = k % VPR * 4, t = k / VPR % kScanTile, which = k / (VPR * kScanTile);
+      if (t < left && n < p.N) {
+        float4 s = *reinterpret_cast<const float4*>(&sm.sum[which][0][t][n]);
 #pragma unroll
         for (int v = 1; v < WARPS; ++v) {
-          const float4 r = *reinterpret_cast<const float4*>(&o.sum[which][v][t][n]);
+          const float4 r = *reinterpret_cast<const float4*>(&sm.sum[which][v][t][n]);
           s = make_float4(__fadd_rn(s.x, r.x), __fadd_rn(s.y, r.y), __fadd_rn(s.z, r.z), __fadd_rn(s.w, r.w));
         }
         const int64_t row = ((int64_t)which * p.nbg + w.blk) * p.B * T + first + t0 + t;
@@ -171,279 +213,223 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC>::THREADS) scan_bwd_kernel(con
     }
   };
 
-  State4 h0[2];
-  load(start(nt - 1));
-  convert(buf[0], start(nt - 1));
-  if (nt > 1) load(start(nt - 2));
-  ld_ckpt(nt - 1, h0);
+  load(nt - 1);
+  States<S> h = ld_ckpt(nt - 1);
+  copy_async_wait();
   __syncthreads();
-  for (int i = nt - 1, cur = 0; i >= 0; --i, cur ^= 1) {
+  for (int i = nt - 1; i >= 0; --i) {
     const int64_t t0 = start(i);
-    if (i + 1 < nt) put_sums(buf[cur ^ 1], start(i + 1));
-    if (i > 0) convert(buf[cur ^ 1], start(i - 1));
-    if (i > 1) load(start(i - 2));
-    Buf& o = buf[cur];
-    State4 h[2] = {h0[0], h0[1]};
-    if (i > 0) ld_ckpt(i - 1, h0);
-    State4 hstart[2] = {h[0], h[1]};
-    // up to the second half
+    const int left = tokens(i);
+    if (i + 1 < nt) put_sums(i + 1);
+    convert(i);
+    __syncthreads();
+    if (i > 0) load(i - 1);
+    st_h(0, h);
+    // up to the last SUB tokens, leaving the states on the way
 #pragma unroll
-    for (int t = 0; t < HALF; ++t) {
-      const float4 dd = o.dd[t][pair];
-      const State4 Bv = lds_state(&o.B[t][4 * g]);
-      scan_absorb(h[0], scan_decay(dd.x, A2[0]), dd.y, Bv);
-      scan_absorb(h[1], scan_decay(dd.z, A2[1]), dd.w, Bv);
+    for (int t = 0; t < kScanTile - SUB; ++t) {
+      const float4 dd = sm.dd[t][pair][order.swap];
+      scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[t][order.perm][S * g]));
+      if ((t + 1) % SUB == 0) st_h((t + 1) / SUB, h);
     }
 #pragma unroll 1
-    for (int half = 1; half >= 0; --half) {
-      const int tb = half * HALF;
-      if (half == 0) {
-        h[0] = hstart[0];
-        h[1] = hstart[1];
-      }
-      State4 a[HALF][2], ah[HALF][2];
-      float sv[8];
+    for (int sub = kScanTile / SUB - 1; sub >= 0; --sub) {
+      const int tb = sub * SUB;
+      {
+        const Row<S> a = ld_row<S>(sm.h[sub][0][tid]), b = ld_row<S>(sm.h[sub][1][tid]);
 #pragma unroll
-      for (int t = 0; t < HALF; t += 2) {
-        float gc[8];
+        for (int j = 0; j < S; ++j) h.n[j] = make_float2(a.n[j], b.n[j]);
+      }
+      // up: the decays and decayed states, gC and s. Nothing is stored before
+      // the end of the sub-block: a store would hold back the shared-memory
+      // loads behind it.
+      States<S> a[SUB], ah[SUB];
+      float gc[SUB / 2][Sums::GV], gb[SUB / 2][Sums::GV], sv[kPairSums<LPC>];
+      float2 s4[SUB];
+#pragma unroll
+      for (int t = 0; t < SUB; t += 2) {
+        float r[2][S];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float4 dd = o.dd[tb + t + u][pair], xv = o.xg[tb + t + u][pair];
-          const State4 Bv = lds_state(&o.B[tb + t + u][4 * g]);
+          const float4 dd = sm.dd[tb + t + u][pair][order.swap];
+          const float2 gs = *reinterpret_cast<const float2*>(&sm.gx[tb + t + u][pair][order.swap]);
+          const Row<S> Bv = ld_row<S>(&sm.B[tb + t + u][order.perm][S * g]);
+          a[t + u] = scan_decay(make_float2(dd.x, dd.y), A2);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float d = k ? dd.z : dd.x, dx = k ? dd.w : dd.y;
-            a[t + u][k] = scan_decay(d, A2[k]);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              ah[t + u][k].q[v] = mul2(a[t + u][k].q[v], h[k].q[v]);
-              h[k].q[v] = fma2(splat2(dx), Bv.q[v], ah[t + u][k].q[v]);
-            }
+          for (int j = 0; j < S; ++j) {
+            ah[t + u].n[j] = mul2(a[t + u].n[j], h.n[j]);
+            h.n[j] = fma2(make_float2(dd.z, dd.w), splat2(Bv.n[j]), ah[t + u].n[j]);
+            const float2 s = mul2(gs, h.n[j]);
+            r[u][j] = __fadd_rn(s.x, s.y);
           }
-          // gC: the sum over channels of gs h
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const float2 s = fma2(splat2(xv.w), h[1].q[v], mul2(splat2(xv.y), h[0].q[v]));
-            gc[4 * u + 2 * v] = s.x;
-            gc[4 * u + 2 * v + 1] = s.y;
-          }
-          if constexpr (Z) {
-            const State4 Cv = lds_state(&o.C[tb + t + u][4 * g]);
-            sv[2 * ((t + u) % 4)] = scan_dot(h[0], Cv);
-            sv[2 * ((t + u) % 4) + 1] = scan_dot(h[1], Cv);
-          }
+          if constexpr (Z) s4[t + u] = scan_dot<S>(h, ld_row<S>(&sm.C[tb + t + u][order.perm][S * g]));
         }
-        reduce_scatter<8, RL, LPC>(gc, lane);
-        const int f = reduce_scatter_first<8, RL>(lane / LPC);
-#pragma unroll
-        for (int v = 0; v < (8 / RL > 0 ? 8 / RL : 1); ++v) o.sum[1][warp][tb + t + (f + v) / 4][4 * g + (f + v) % 4] = gc[v];
-        if constexpr (Z) {
-          if (t % 4 == 2) {
-            // s, and with it gz, of 4 tokens
-            reduce_scatter<8, LPC>(sv, lane);
-            const int f2 = reduce_scatter_first<8, LPC>(g);
-#pragma unroll
-            for (int v = 0; v < (8 / LPC > 0 ? 8 / LPC : 1); ++v) {
-              const int tt = tb + t - 2 + (f2 + v) / 2, k = (f2 + v) % 2;
-              const float4 xv = o.xg[tt][pair], zv = o.sz[tt][pair];
-              const float s = __fmaf_rn(k ? D[1] : D[0], k ? xv.z : xv.x, sv[v]);
-              if (t0 + tt < tend && ch_on && g < 8)
-                gzg[(t0 + tt) * p.C + c + k] = Elem<E>::from_f32(__fmul_rn(k ? zv.w : zv.y, s));
-            }
-          }
-        }
+        Sums::sum(r, gc[t / 2], lane);
       }
+      if constexpr (Z) pair_sums<LPC>(s4, sv, lane);
       // down again
+      float2 qb[SUB], wa[SUB];  // sum Q B, sum A2 Q a h
 #pragma unroll
-      for (int t = HALF - TG; t >= 0; t -= TG) {
-        float out[4 * TG];  // token, channel, (sum Q B, sum A2 Q a h)
+      for (int t = SUB - 2; t >= 0; t -= 2) {
+        float r[2][S];
 #pragma unroll
-        for (int u = TG - 1; u >= 0; --u) {
+        for (int u = 1; u >= 0; --u) {
           const int tt = tb + t + u;
-          const float4 dd = o.dd[tt][pair], xv = o.xg[tt][pair];
-          const State4 Bv = lds_state(&o.B[tt][4 * g]), Cv = lds_state(&o.C[tt][4 * g]);
-          State4 Q[2];
+          const float4 dd = sm.dd[tt][pair][order.swap];
+          const float2 gs = *reinterpret_cast<const float2*>(&sm.gx[tt][pair][order.swap]);
+          const Row<S> Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
+          States<S> Q, W;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float d = k ? dd.z : dd.x, gs = k ? xv.w : xv.y;
-            State4 W;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              Q[k].q[v] = fma2(splat2(gs), Cv.q[v], q[k].q[v]);
-              q[k].q[v] = mul2(a[t + u][k].q[v], Q[k].q[v]);
-              W.q[v] = mul2(Q[k].q[v], ah[t + u][k].q[v]);
-              gA[k].q[v] = fma2(splat2(d), W.q[v], gA[k].q[v]);
-            }
-            out[4 * u + 2 * k] = scan_dot(Q[k], Bv);
-            out[4 * u + 2 * k + 1] = scan_dot(W, A2[k]);
+          for (int j = 0; j < S; ++j) {
+            Q.n[j] = fma2(gs, splat2(Cv.n[j]), q.n[j]);
+            q.n[j] = mul2(a[t + u].n[j], Q.n[j]);
+            W.n[j] = mul2(Q.n[j], ah[t + u].n[j]);
+            gA.n[j] = fma2(make_float2(dd.x, dd.y), W.n[j], gA.n[j]);
+            const float2 s = mul2(make_float2(dd.z, dd.w), Q.n[j]);
+            r[u][j] = __fadd_rn(s.x, s.y);
           }
-          // gB of this token: keep Q's channel sum in place of a (used up)
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-            a[t + u][0].q[v] = fma2(splat2(dd.w), Q[1].q[v], mul2(splat2(dd.y), Q[0].q[v]));
+          qb[t + u] = scan_dot<S>(Q, ld_row<S>(&sm.B[tt][order.perm][S * g]));
+          wa[t + u] = scan_dot<S>(W, A2);
         }
+        Sums::sum(r, gb[t / 2], lane);
+      }
+      float out[kPairSums<LPC>], out2[kPairSums<LPC>];
+      pair_sums<LPC>(qb, out, lane);
+      pair_sums<LPC>(wa, out2, lane);
+      // the sub-block's results
 #pragma unroll
-        for (int u = 0; u < TG; u += 2) {
-          float gb[8];
+      for (int t = 0; t < SUB; t += 2)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              gb[4 * e + 2 * v] = a[t + u + e][0].q[v].x;
-              gb[4 * e + 2 * v + 1] = a[t + u + e][0].q[v].y;
-            }
-          reduce_scatter<8, RL, LPC>(gb, lane);
-          const int f = reduce_scatter_first<8, RL>(lane / LPC);
-#pragma unroll
-          for (int v = 0; v < (8 / RL > 0 ? 8 / RL : 1); ++v)
-            o.sum[0][warp][tb + t + u + (f + v) / 4][4 * g + (f + v) % 4] = gb[v];
+        for (int v = 0; v < Sums::GV; ++v) {
+          const int tt = tb + t + Sums::token(v, lane), n = S * g + ((v % Sums::GS) ^ order.perm);
+          sm.sum[1][warp][tt][n] = gc[t / 2][v];
+          sm.sum[0][warp][tt][n] = gb[t / 2][v];
         }
-        reduce_scatter<4 * TG, LPC>(out, lane);
-        const int f = reduce_scatter_first<4 * TG, LPC>(g);
+      const int64_t at = (first + t0) * p.C + c + order.swap;
 #pragma unroll
-        for (int v = 0; v < 4 * TG / LPC; v += 2) {
-          const int tt = tb + t + (f + v) / 4, k = (f + v) % 4 / 2;
-          const float4 dd = o.dd[tt][pair], xv = o.xg[tt][pair], zv = o.sz[tt][pair];
-          const float d = k ? dd.z : dd.x, x = k ? xv.z : xv.x, gs = k ? xv.w : xv.y;
-          const float gx = __fmaf_rn(out[v], d, __fmul_rn(gs, k ? D[1] : D[0]));
-          const float gd = __fmaf_rn(out[v], x, __fmul_rn(out[v + 1], 1.f / kLog2e));
-          const float graw = __fmul_rn(gd, k ? zv.z : zv.x);
-          if (t0 + tt < tend && ch_on) {
-            gxg[(t0 + tt) * p.C + c + k] = Elem<E>::from_f32(gx);
-            gdtg[(t0 + tt) * p.C + c + k] = Elem<E>::from_f32(graw);
-          }
-          const float gdx = __fmul_rn(gs, x);
-          if (k) {
-            gD[1] = __fadd_rn(gD[1], gdx);
-            gdb[1] = __fadd_rn(gdb[1], graw);
-          } else {
-            gD[0] = __fadd_rn(gD[0], gdx);
-            gdb[0] = __fadd_rn(gdb[0], graw);
-          }
+      for (int v = 0; v < kPairSums<LPC>; ++v) {
+        const int tt = tb + pair_sum_first<LPC>(g) + v;
+        const float d = sm.dd[tt][pair][order.swap].x;
+        const float4 gx = sm.gx[tt][pair][order.swap];
+        const float2 sz = sm.sz[tt][pair][order.swap];
+        const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gx.x, D));
+        const float graw = __fmul_rn(__fmaf_rn(out[v], gx.z, __fmul_rn(out2[v], 1.f / kLog2e)), sz.x);
+        if (tt < left && ch_on && g < 8) {
+          static_cast<E*>(p.gx)[at + tt * p.C] = Elem<E>::from_f32(rgx);
+          static_cast<E*>(p.gdt)[at + tt * p.C] = Elem<E>::from_f32(graw);
+          if constexpr (Z)
+            static_cast<E*>(p.gz)[at + tt * p.C] = Elem<E>::from_f32(__fmul_rn(sz.y, __fmaf_rn(D, gx.z, sv[v])));
+          gD = __fmaf_rn(gx.x, gx.z, gD);
+          gdb = __fadd_rn(gdb, graw);
         }
       }
     }
+    if (i > 0) h = ld_ckpt(i - 1);
+    copy_async_wait();
     __syncthreads();
   }
-  put_sums(buf[(nt - 1) & 1], start(0));
+  put_sums(0);
 
   const int64_t prow = w.b * p.nseg + w.seg;
+  if (on) st_states<S>(p.part_a + (prow * p.C + c) * p.N + S * g, p.N, gA, order);
+  if (on && p.g_init && w.seg == 0) st_states<S>(p.g_init + state_at, p.N, q, order);
+  // over the lanes of the channel, each of which finished other tokens
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (on) st_state(p.part_a + (prow * p.C + c + k) * p.N + 4 * g, gA[k]);
-    if (on && p.g_init && w.seg == 0) st_state(p.g_init + (w.b * p.C + c + k) * p.N + 4 * g, q[k]);
-    // over the lanes of the channel, each of which finished other tokens
-#pragma unroll
-    for (int m = 1; m < LPC; m *= 2) {
-      gD[k] = __fadd_rn(gD[k], __shfl_xor_sync(0xffffffffu, gD[k], m));
-      gdb[k] = __fadd_rn(gdb[k], __shfl_xor_sync(0xffffffffu, gdb[k], m));
-    }
-    if (ch_on && g == 0) {
-      p.part_d[prow * p.C + c + k] = gD[k];
-      p.part_d[(p.B * p.nseg + prow) * p.C + c + k] = gdb[k];
-    }
+  for (int m = 2; m < LPC; m *= 2) {
+    gD = __fadd_rn(gD, __shfl_xor_sync(0xffffffffu, gD, m));
+    gdb = __fadd_rn(gdb, __shfl_xor_sync(0xffffffffu, gdb, m));
+  }
+  if (ch_on && g < 2) {
+    p.part_d[prow * p.C + c + g] = gD;
+    p.part_d[(p.B * p.nseg + prow) * p.C + c + g] = gdb;
   }
 }
 
 // What a piece, walked down from Q = 0, hands to the piece below, and its sum of d.
-template <int CB, int NP>
-struct BwdCarryBuf {
-  float4 dg[kScanTile][CB / 2];  // d0, gs0, d1, gs1
-  float C[kScanTile][NP];
+template <class E, class Geo>
+struct ScanBwdCarryShared {
+  ScanRaw<E, Geo, kActs> raw[2];
+  float4 dg[2][kScanTile][Geo::HB];  // d0, d1, gs0, gs1
+  float C[2][kScanTile][Geo::NP];
 };
-template <class E, int LPC>
-__global__ void __launch_bounds__(ScanGeom<E, LPC>::THREADS) scan_bwd_carry_kernel(const ScanParams p) {
-  using Geo = ScanGeom<E, LPC>;
-  constexpr int CB = Geo::CB, VN = Geo::VN;
-  __shared__ BwdCarryBuf<CB, Geo::NP> buf[2];
-  const ScanPlace w = scan_place<CB>(p);
+template <class E, int LPC, int S>
+__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_bwd_carry_kernel(const ScanParams p) {
+  using Geo = ScanGeom<E, LPC, S>;
+  extern __shared__ float4 smem4[];
+  auto& sm = *reinterpret_cast<ScanBwdCarryShared<E, Geo>*>(smem4);
+  const ScanPlace w = scan_place<Geo::CB>(p);
   if (w.seg == 0) return;  // nothing lies below the first piece
   const int tid = threadIdx.x;
   const int64_t first = w.b * p.T;
   const int64_t tbeg = w.seg * p.seg_tokens;
   const int64_t tend = w.seg == p.nseg - 1 ? p.T : tbeg + p.seg_tokens;
-  const E* dtg = static_cast<const E*>(p.dt) + first * p.C;
-  const E* gyg = static_cast<const E*>(p.gy) + first * p.C;
-  const E* zg = p.z ? static_cast<const E*>(p.z) + first * p.C : nullptr;
-  const int64_t GN = p.G * p.N, gN = w.g * p.N;
-  const E* Cg = static_cast<const E*>(p.Cm) + first * GN;
-  const int col = tid % Geo::VPR * VN;
-  const bool col_on = w.c0 + col < w.cend;
-  float bias[VN];
-  ld_param<VN>(p.dt_bias && col_on ? p.dt_bias + w.c0 + col : nullptr, bias, 0.f);
-  ScanRows<E, LPC> rdt, rz, rgy;
-  ScanVecs<E, LPC> rc;
-  auto load = [&](int64_t t0) {
-    rdt.load(dtg, t0, tend, p.C, w.c0, w.cend);
-    rgy.load(gyg, t0, tend, p.C, w.c0, w.cend);
-    if (zg) rz.load(zg, t0, tend, p.C, w.c0, w.cend);
-    rc.load(Cg, t0, tend, GN, gN, p.N);
+  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
+  const int64_t GN = p.G * p.N;
+  const int channels = (int)(w.cend - w.c0);
+  auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
+  auto tokens = [&](int i) { return (int)min(tend - start(i), (int64_t)kScanTile); };
+  auto load = [&](int i) {
+    ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+    const int left = tokens(i);
+    const int64_t at = (first + start(i)) * p.C + w.c0;
+    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
+    r.load_act(kActGy, static_cast<const E*>(p.gy), at, p.C, left, channels);
+    if (p.z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
+    r.load_bc(1, static_cast<const E*>(p.Cm), (first + start(i)) * GN + w.g * p.N, GN, left, (int)p.N);
+    copy_async_commit();
   };
-  auto convert = [&](BwdCarryBuf<CB, Geo::NP>& o, int64_t t0) {
-    rc.put(&o.C[0][0]);
+  const int lp = tid % Geo::HB;
+  const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);
+  auto convert = [&](int i) {
+    const ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+    const int left = tokens(i);
+    r.template put_bc<1>(1, &sm.C[i & 1][0][0]);
 #pragma unroll
-    for (int i = 0; i < Geo::PT; ++i) {
-      const int t = (tid + i * Geo::THREADS) / Geo::VPR;
-      if (t < kScanTile) {
-        float dt[VN], z[VN], gs[VN];
-        rdt.v[i].get(dt);
-        rgy.v[i].get(gs);
-        if (zg) rz.v[i].get(z);
-#pragma unroll
-        for (int n = 0; n < VN; ++n) {
-          dt[n] = t0 + t < tend ? scan_step_size(dt[n], bias[n], p.softplus) : 0.f;
-          if (zg) gs[n] = __fmul_rn(gs[n], __fmul_rn(z[n], sigmoid_f(z[n])));
-        }
-#pragma unroll
-        for (int n = 0; n < VN; n += 2) o.dg[t][(col + n) / 2] = make_float4(dt[n], gs[n], dt[n + 1], gs[n + 1]);
+    for (int j = 0; j < Geo::PT; ++j) {
+      const int t = tid / Geo::HB + j * Geo::ROWS;
+      const float2 d = t < left ? scan_step_size2(ld_pair(&r.act[kActDt][t][2 * lp]), bias, p.softplus) : splat2(0.f);
+      float2 gs = ld_pair(&r.act[kActGy][t][2 * lp]);
+      if (p.z) {
+        const float2 z = ld_pair(&r.act[kActZ][t][2 * lp]);
+        gs = mul2(gs, mul2(z, sigmoid2(z)));
       }
+      sm.dg[i & 1][t][lp] = make_float4(d.x, d.y, gs.x, gs.y);
     }
   };
   const int pair = tid / LPC, g = tid % LPC;
   const int64_t c = w.c0 + 2 * pair;
-  const bool on = c < w.cend && 4 * g < p.N;
-  State4 A2[2], q[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    A2[k] = scale4(ld_state(p.A + (c + k) * p.N + 4 * g, on), kLog2e);
-    q[k].q[0] = q[k].q[1] = splat2(0.f);
-  }
-  float sum_d[2] = {0.f, 0.f};
-  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
-  auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
-  load(start(nt - 1));
-  convert(buf[0], start(nt - 1));
-  if (nt > 1) load(start(nt - 2));
+  const bool on = 2 * pair < channels && S * g < p.N;
+  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, on), kLog2e);
+  States<S> q = ld_states_wide<S>(nullptr, 0, false);
+  float2 sum_d = splat2(0.f);
+  load(nt - 1);
+  if (nt > 1) load(nt - 2);
+  copy_async_wait();
   __syncthreads();
-  for (int i = nt - 1, cur = 0; i >= 0; --i, cur ^= 1) {
-    if (i > 0) convert(buf[cur ^ 1], start(i - 1));
-    if (i > 1) load(start(i - 2));
-    const auto& o = buf[cur];
-    float tile_d[2] = {0.f, 0.f};
+  convert(nt - 1);
+  __syncthreads();
+  for (int i = nt - 1; i >= 0; --i) {
+    if (i > 1) load(i - 2);
+    if (i > 0) convert(i - 1);
+    const int o = i & 1;
+    float2 tile_d = splat2(0.f);
 #pragma unroll
     for (int t = kScanTile - 1; t >= 0; --t) {
-      const float4 dg = o.dg[t][pair];
-      const State4 Cv = lds_state(&o.C[t][4 * g]);
+      const float4 dg = sm.dg[o][t][pair];
+      const Row<S> Cv = ld_row<S>(&sm.C[o][t][S * g]);
+      const float2 d = make_float2(dg.x, dg.y);
+      const States<S> a = scan_decay(d, A2);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float d = k ? dg.z : dg.x, gs = k ? dg.w : dg.y;
-        const State4 a = scan_decay(d, A2[k]);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) q[k].q[v] = mul2(a.q[v], fma2(splat2(gs), Cv.q[v], q[k].q[v]));
-        tile_d[k] = __fadd_rn(tile_d[k], d);
-      }
+      for (int j = 0; j < S; ++j) q.n[j] = mul2(a.n[j], fma2(make_float2(dg.z, dg.w), splat2(Cv.n[j]), q.n[j]));
+      tile_d = add2(tile_d, d);
     }
-    sum_d[0] = __fadd_rn(sum_d[0], tile_d[0]);
-    sum_d[1] = __fadd_rn(sum_d[1], tile_d[1]);
+    sum_d = add2(sum_d, tile_d);
+    copy_async_wait();
     __syncthreads();
   }
   const int64_t row = (w.b * p.nseg + w.seg) * p.C + c;
-  float* sums = p.carry + p.B * p.nseg * p.C * p.N;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (on) st_state(p.carry + (row + k) * p.N + 4 * g, q[k]);
-    if (on && g == 0) sums[row + k] = sum_d[k];
-  }
+  if (on) st_states_wide<S>(p.carry + row * p.N + S * g, p.N, q, 0);
+  if (on && g == 0) st_pair(p.carry + p.B * p.nseg * p.C * p.N + row, sum_d);
 }
 
 // gB and gC: the sum of the CTAs' partial rows, in order, in the storage type.
@@ -470,34 +456,37 @@ wkv_status launched(const char* what, const char** why) {
   return WKV_ERR_CUDA;
 }
 
-template <class E, int LPC, bool Z>
-wkv_status run_main(const ScanParams& p, cudaStream_t st, const char** why) {
-  using Geo = ScanGeom<E, LPC>;
-  constexpr size_t smem = 2 * sizeof(BwdBuf<Geo::CB, Geo::NP, Geo::THREADS / 32>);
-  static_assert(smem <= 227 * 1024, "the tiles fit an SM");
-  if (cudaFuncSetAttribute(scan_bwd_kernel<E, LPC, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess) {
-    *why = "scan backward kernel: shared memory request failed";
+// A kernel with more than the static limit of shared memory.
+template <class K>
+wkv_status run_shared(K kernel, const ScanParams& p, int threads, size_t smem, cudaStream_t st, const char* what,
+                      const char** why) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    *why = what;
     return WKV_ERR_CUDA;
   }
-  const int64_t grid = p.B * p.nseg * p.G * p.nbg;
-  scan_bwd_kernel<E, LPC, Z><<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
-  return launched("scan backward kernel launch failed", why);
+  kernel<<<(unsigned)(p.B * p.nseg * p.G * p.nbg), threads, smem, st>>>(p);
+  return launched(what, why);
 }
 
-template <class E, int LPC>
+template <class E, int LPC, int S>
 wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why) {
   const ScanArgs& a = b.f;
   const ScanCut cut = scan_bwd_cut(a.B, a.T, a.C, a.N, a.G);
   ScanParams p = scan_params(a, cut);
   p.gy = b.gy, p.g_final = b.g_final, p.gx = b.gx, p.gdt = b.gdt, p.gz = b.gz, p.g_init = b.g_init;
   p.part_bc = b.part_bc, p.part_a = b.part_a, p.part_d = b.part_d;
-  if (cut.nseg > 1) {
-    const int64_t grid = p.B * p.nseg * p.G * p.nbg;
-    scan_bwd_carry_kernel<E, LPC><<<(unsigned)grid, ScanGeom<E, LPC>::THREADS, 0, st>>>(p);
-    if (wkv_status s = launched("scan backward carry kernel launch failed", why)) return s;
-  }
-  if (wkv_status s = a.z ? run_main<E, LPC, true>(p, st, why) : run_main<E, LPC, false>(p, st, why)) return s;
+  using Geo = ScanGeom<E, LPC, S>;
+  constexpr size_t smem = sizeof(ScanBwdShared<E, Geo>);
+  static_assert(smem <= 227 * 1024, "the tiles fit an SM");
+  if (cut.nseg > 1)
+    if (wkv_status s = run_shared(scan_bwd_carry_kernel<E, LPC, S>, p, Geo::THREADS, sizeof(ScanBwdCarryShared<E, Geo>), st,
+                                  "scan backward carry kernel launch failed", why))
+      return s;
+  if (wkv_status s = a.z ? run_shared(scan_bwd_kernel<E, LPC, S, true>, p, Geo::THREADS, smem, st,
+                                      "scan backward kernel launch failed", why)
+                         : run_shared(scan_bwd_kernel<E, LPC, S, false>, p, Geo::THREADS, smem, st,
+                                      "scan backward kernel launch failed", why))
+    return s;
   const int64_t n4 = a.B * a.T * a.G * a.N / 4;
   scan_sum_bc_kernel<E><<<dim3((unsigned)ceil_div(n4, 256), 2), 256, 0, st>>>(b.part_bc, p.nbg, n4, static_cast<E*>(b.gB),
                                                                             static_cast<E*>(b.gC));
@@ -512,13 +501,17 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
 }  // namespace
 
 wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const char** why) {
+#ifdef WKV_QUICK
+  return run_backward<__nv_bfloat16, 8, 2>(a, stream, why);
+#else
   const bool bf = a.f.dtype == WKV_BF16;
-  switch (scan_lanes(a.f.N)) {
-    case 2: return bf ? run_backward<__nv_bfloat16, 2>(a, stream, why) : run_backward<float, 2>(a, stream, why);
-    case 4: return bf ? run_backward<__nv_bfloat16, 4>(a, stream, why) : run_backward<float, 4>(a, stream, why);
-    case 8: return bf ? run_backward<__nv_bfloat16, 8>(a, stream, why) : run_backward<float, 8>(a, stream, why);
-    default: return bf ? run_backward<__nv_bfloat16, 16>(a, stream, why) : run_backward<float, 16>(a, stream, why);
+  switch (scan_padded_states(a.f.N)) {
+    case 8: return bf ? run_backward<__nv_bfloat16, 4, 2>(a, stream, why) : run_backward<float, 4, 2>(a, stream, why);
+    case 16: return bf ? run_backward<__nv_bfloat16, 8, 2>(a, stream, why) : run_backward<float, 8, 2>(a, stream, why);
+    case 32: return bf ? run_backward<__nv_bfloat16, 8, 4>(a, stream, why) : run_backward<float, 8, 4>(a, stream, why);
+    default: return bf ? run_backward<__nv_bfloat16, 16, 4>(a, stream, why) : run_backward<float, 16, 4>(a, stream, why);
   }
+#endif
 }
 
 }  // namespace wkv

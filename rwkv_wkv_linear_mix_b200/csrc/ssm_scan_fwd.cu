@@ -27,22 +27,22 @@ namespace {
 
 enum ScanMode { kScanMain, kScanCarry, kScanSlots };
 
-template <int CB, int NP>
-struct ScanBuf {
-  float4 dd[kScanTile][CB / 2];  // per channel pair: d0, d0 x0, d1, d1 x1
-  float4 eg[kScanTile][CB / 2];  // D0 x0, gate0, D1 x1, gate1
-  float B[kScanTile][NP];
-  float C[kScanTile][NP];
+enum { kActX, kActDt, kActZ, kActs };
+
+template <class E, class Geo>
+struct ScanFwdShared {
+  ScanRaw<E, Geo, kActs> raw[2];         // the tile at work, and the next in flight
+  float4 dd[kScanTile][Geo::HB][2];      // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
+  float B[kScanTile][Geo::NP];
+  float C[kScanTile][Geo::NP];
 };
 
-template <class E, int LPC, int MODE>
-__global__ void __launch_bounds__(ScanGeom<E, LPC>::THREADS) scan_fwd_kernel(const ScanParams p) {
-  using Geo = ScanGeom<E, LPC>;
-  constexpr int CB = Geo::CB, NP = Geo::NP, VN = Geo::VN;
-  using Buf = ScanBuf<CB, NP>;
+template <class E, int LPC, int S, int MODE>
+__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_fwd_kernel(const ScanParams p) {
+  using Geo = ScanGeom<E, LPC, S>;
   extern __shared__ float4 smem4[];
-  Buf* buf = reinterpret_cast<Buf*>(smem4);
-  const ScanPlace w = scan_place<CB>(p);
+  auto& sm = *reinterpret_cast<ScanFwdShared<E, Geo>*>(smem4);
+  const ScanPlace w = scan_place<Geo::CB>(p);
   const int tid = threadIdx.x;
   if (MODE == kScanCarry && w.seg == p.nseg - 1) return;  // nothing follows the last piece
   int64_t first = w.b * p.T, T = p.T;
@@ -58,200 +58,161 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC>::THREADS) scan_fwd_kernel(con
   }
   const int64_t tbeg = w.seg * p.seg_tokens;
   const int64_t tend = MODE == kScanSlots || w.seg == p.nseg - 1 ? T : tbeg + p.seg_tokens;
-  const E* xg = static_cast<const E*>(p.x) + first * p.C;
-  const E* dtg = static_cast<const E*>(p.dt) + first * p.C;
-  const E* zg = p.z ? static_cast<const E*>(p.z) + first * p.C : nullptr;
-  E* yg = static_cast<E*>(p.y);
-  if (yg) yg += first * p.C;
-  const int64_t GN = p.G * p.N, gN = w.g * p.N;
-  const E* Bg = static_cast<const E*>(p.Bm) + first * GN;
-  const E* Cg = static_cast<const E*>(p.Cm) + first * GN;
+  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
+  const int64_t GN = p.G * p.N;
+  const int channels = (int)(w.cend - w.c0);
 
-  // the thread's channels in the loads, and their parameters
-  const int col = tid % Geo::VPR * VN;
-  const bool col_on = w.c0 + col < w.cend;
-  float bias[VN], Dv[VN];
-  ld_param<VN>(p.dt_bias && col_on ? p.dt_bias + w.c0 + col : nullptr, bias, 0.f);
-  ld_param<VN>(MODE != kScanCarry && p.D && col_on ? p.D + w.c0 + col : nullptr, Dv, 0.f);
-
-  ScanRows<E, LPC> rx, rdt, rz;
-  ScanVecs<E, LPC> rb, rc;
-  auto load = [&](int64_t t0) {
-    rx.load(xg, t0, tend, p.C, w.c0, w.cend);
-    rdt.load(dtg, t0, tend, p.C, w.c0, w.cend);
-    rb.load(Bg, t0, tend, GN, gN, p.N);
+  auto load = [&](int i) {
+    ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+    const int64_t t0 = tbeg + (int64_t)i * kScanTile;
+    const int left = (int)min(tend - t0, (int64_t)kScanTile);
+    const int64_t at = (first + t0) * p.C + w.c0, bc = (first + t0) * GN + w.g * p.N;
+    r.load_act(kActX, static_cast<const E*>(p.x), at, p.C, left, channels);
+    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
+    r.load_bc(0, static_cast<const E*>(p.Bm), bc, GN, left, (int)p.N);
     if constexpr (MODE != kScanCarry) {
-      rc.load(Cg, t0, tend, GN, gN, p.N);
-      if (zg) rz.load(zg, t0, tend, p.C, w.c0, w.cend);
+      r.load_bc(1, static_cast<const E*>(p.Cm), bc, GN, left, (int)p.N);
+      if (p.z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
     }
+    copy_async_commit();
   };
-  auto convert = [&](Buf& o, int64_t t0) {
-    rb.put(&o.B[0][0]);
-    if constexpr (MODE != kScanCarry) rc.put(&o.C[0][0]);
+  // the thread's channel pair in the conversion
+  const int lp = tid % Geo::HB;
+  const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);
+  auto convert = [&](int i) {
+    const ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+    r.template put_bc<1>(0, &sm.B[0][0]);
+    if constexpr (MODE != kScanCarry) r.template put_bc<1>(1, &sm.C[0][0]);
+    const int left = (int)min(tend - tbeg - (int64_t)i * kScanTile, (int64_t)kScanTile);
 #pragma unroll
-    for (int i = 0; i < Geo::PT; ++i) {
-      const int t = (tid + i * Geo::THREADS) / Geo::VPR;
-      if (t < kScanTile) {
-        const bool real = t0 + t < tend;
-        float x[VN], dt[VN], z[VN];
-        rx.v[i].get(x);
-        rdt.v[i].get(dt);
-        if (MODE != kScanCarry && zg) rz.v[i].get(z);
-#pragma unroll
-        for (int n = 0; n < VN; n += 2) {
-          float d[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // a token past the end: d = 0 leaves the state as it is
-            d[k] = real ? scan_step_size(dt[n + k], bias[n + k], p.softplus) : 0.f;
-          }
-          o.dd[t][(col + n) / 2] = make_float4(d[0], __fmul_rn(d[0], x[n]), d[1], __fmul_rn(d[1], x[n + 1]));
-          if constexpr (MODE != kScanCarry) {
-            const float g0 = zg ? __fmul_rn(z[n], sigmoid_f(z[n])) : 1.f;
-            const float g1 = zg ? __fmul_rn(z[n + 1], sigmoid_f(z[n + 1])) : 1.f;
-            o.eg[t][(col + n) / 2] = make_float4(__fmul_rn(Dv[n], x[n]), g0, __fmul_rn(Dv[n + 1], x[n + 1]), g1);
-          }
-        }
-      }
+    for (int j = 0; j < Geo::PT; ++j) {
+      const int t = tid / Geo::HB + j * Geo::ROWS;
+      // a token past the end: d = 0 leaves the state as it is
+      const float2 d = t < left ? scan_step_size2(ld_pair(&r.act[kActDt][t][2 * lp]), bias, p.softplus) : splat2(0.f);
+      const float2 dx = mul2(d, ld_pair(&r.act[kActX][t][2 * lp]));
+      sm.dd[t][lp][0] = make_float4(d.x, d.y, dx.x, dx.y);
+      sm.dd[t][lp][1] = make_float4(d.y, d.x, dx.y, dx.x);
     }
   };
 
   // the thread's channel pair and states
-  const int pair = tid / LPC, g = tid % LPC;
+  const int pair = tid / LPC, g = tid % LPC, swap = g & 1;
+  const LaneOrder order{swap, 0};
   const int64_t c = w.c0 + 2 * pair;
-  const bool on = c < w.cend && 4 * g < p.N;  // channel counts are even
-  State4 A2[2], h[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    A2[k] = scale4(ld_state(p.A + (c + k) * p.N + 4 * g, on), kLog2e);
-    h[k] = ld_state(p.init_state + (w.b * p.C + c + k) * p.N + 4 * g, MODE != kScanCarry && on && p.init_state);
-  }
+  const bool ch_on = 2 * pair < channels, on = ch_on && S * g < p.N;  // channel counts are even
+  const States<S> A2 = scale_states<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order), kLog2e);
+  const float D = MODE != kScanCarry && p.D && ch_on ? p.D[c + swap] : 0.f;
+  const int64_t state_at = (w.b * p.C + c) * p.N + S * g;
+  States<S> h = ld_states<S>(p.init_state + state_at, p.N, MODE != kScanCarry && on && p.init_state, order);
   if constexpr (MODE == kScanMain) {
     const float* sums = p.carry + p.B * p.nseg * p.C * p.N;
     for (int j = 0; j < w.seg; ++j) {
-      const int64_t row = (w.b * p.nseg + j) * p.C + c;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (on) {
-          const State4 s = ld_state(p.carry + (row + k) * p.N + 4 * g, true);
-          const State4 a = scan_decay(sums[row + k], A2[k]);
-          h[k].q[0] = fma2(a.q[0], h[k].q[0], s.q[0]);
-          h[k].q[1] = fma2(a.q[1], h[k].q[1], s.q[1]);
-        }
+      if (on) {
+        const int64_t row = (w.b * p.nseg + j) * p.C + c;
+        const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
+        scan_fold(h, scan_decay(make_float2(sums[row + swap], sums[row + 1 - swap]), A2), s);
       }
     }
   }
-  float sum_d[2] = {0.f, 0.f};
-  const int out0 = reduce_scatter_first<8, LPC>(g);
+  float2 sum_d = splat2(0.f);
+  const int out0 = pair_sum_first<LPC>(g);
 
-  const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
-  load(tbeg);
-  convert(buf[0], tbeg);
-  if (nt > 1) load(tbeg + kScanTile);
+  load(0);
+  copy_async_wait();
   __syncthreads();
   for (int i = 0; i < nt; ++i) {
     const int64_t t0 = tbeg + (int64_t)i * kScanTile;
-    if (i + 1 < nt) convert(buf[(i + 1) & 1], t0 + kScanTile);
-    if (i + 2 < nt) load(t0 + 2 * kScanTile);
-    const Buf& o = buf[i & 1];
+    if (i + 1 < nt) load(i + 1);
+    convert(i);
+    __syncthreads();
     if (MODE == kScanMain && p.ckpt && on) {
       const int64_t m = t0 / kScanTile, nck = (p.T + kScanTile - 1) / kScanTile;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) st_state(p.ckpt + ((w.b * nck + m) * p.C + c + k) * p.N + 4 * g, h[k]);
+      st_states_wide<S>(p.ckpt + ((w.b * nck + m) * p.C + c) * p.N + S * g, p.N, h, swap);
     }
-    float tile_d[2] = {0.f, 0.f};
+    float2 tile_d = splat2(0.f);
+    float done[kScanTile / 4][kPairSums<LPC>];  // stored after the walk: a store would hold back the loads behind it
 #pragma unroll
     for (int tg = 0; tg < kScanTile; tg += 4) {
-      float out[8];
+      float2 out[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 dd = o.dd[tg + j][pair];
-        const State4 Bv = lds_state(&o.B[tg + j][4 * g]);
-        scan_absorb(h[0], scan_decay(dd.x, A2[0]), dd.y, Bv);
-        scan_absorb(h[1], scan_decay(dd.z, A2[1]), dd.w, Bv);
-        if constexpr (MODE != kScanCarry) {
-          const State4 Cv = lds_state(&o.C[tg + j][4 * g]);
-          out[2 * j] = scan_dot(h[0], Cv);
-          out[2 * j + 1] = scan_dot(h[1], Cv);
-        } else {
-          tile_d[0] = __fadd_rn(tile_d[0], dd.x);
-          tile_d[1] = __fadd_rn(tile_d[1], dd.z);
-        }
+        const float4 dd = sm.dd[tg + j][pair][swap];
+        const float2 d = make_float2(dd.x, dd.y);
+        scan_absorb(h, scan_decay(d, A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[tg + j][S * g]));
+        if constexpr (MODE != kScanCarry)
+          out[j] = scan_dot<S>(h, ld_row<S>(&sm.C[tg + j][S * g]));
+        else
+          tile_d = add2(tile_d, d);
       }
-      if constexpr (MODE != kScanCarry) {
-        reduce_scatter<8, LPC>(out, tid);
-        // out[i] is now value out0 + i: token (out0 + i) / 2, channel (out0 + i) % 2
-        if constexpr (LPC <= 4) {
+      if constexpr (MODE != kScanCarry) pair_sums<LPC>(out, done[tg / 4], tid);
+    }
+    if (MODE != kScanCarry && p.y) {
+      // done[tg / 4][v]: channel `swap` of token tg + out0 + v
+      const int left = ch_on && g < 8 ? (int)min(tend - t0, (int64_t)kScanTile) : 0;
+      const ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+      E* y = static_cast<E*>(p.y) + (first + t0) * p.C + c + swap;
 #pragma unroll
-          for (int v = 0; v < 8 / LPC; v += 2) {
-            const int t = tg + (out0 + v) / 2;
-            const float4 e = o.eg[t][pair];
-            const float2 y = make_float2(__fmul_rn(__fadd_rn(out[v], e.x), e.y), __fmul_rn(__fadd_rn(out[v + 1], e.z), e.w));
-            if (yg && t0 + t < tend && c < w.cend) st_pair(yg + (t0 + t) * p.C + c, y);
+      for (int tg = 0; tg < kScanTile; tg += 4) {
+#pragma unroll
+        for (int v = 0; v < kPairSums<LPC>; ++v) {
+          const int t = tg + out0 + v;
+          float o = __fadd_rn(done[tg / 4][v], __fmul_rn(D, Elem<E>::to_f32(r.act[kActX][t][2 * pair + swap])));
+          if (p.z) {
+            const float z = Elem<E>::to_f32(r.act[kActZ][t][2 * pair + swap]);
+            o = __fmul_rn(o, __fmul_rn(z, sigmoid_f(z)));
           }
-        } else {
-          const int t = tg + out0 / 2, k = out0 % 2;
-          const float4 e = o.eg[t][pair];
-          const float y = __fmul_rn(__fadd_rn(out[0], k ? e.z : e.x), k ? e.w : e.y);
-          if (yg && t0 + t < tend && c < w.cend && g < 8) yg[(t0 + t) * p.C + c + k] = Elem<E>::from_f32(y);
+          if (t < left) y[t * p.C] = Elem<E>::from_f32(o);
         }
       }
     }
-    sum_d[0] = __fadd_rn(sum_d[0], tile_d[0]);
-    sum_d[1] = __fadd_rn(sum_d[1], tile_d[1]);
+    sum_d = add2(sum_d, tile_d);
+    copy_async_wait();
     __syncthreads();
   }
   if constexpr (MODE == kScanCarry) {
     const int64_t row = (w.b * p.nseg + w.seg) * p.C + c;
-    float* sums = p.carry + p.B * p.nseg * p.C * p.N;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (on) st_state(p.carry + (row + k) * p.N + 4 * g, h[k]);
-      if (on && g == 0) sums[row + k] = sum_d[k];
-    }
+    if (on) st_states_wide<S>(p.carry + row * p.N + S * g, p.N, h, swap);
+    if (on && g == 0) st_pair(p.carry + p.B * p.nseg * p.C * p.N + row, sum_d);
   } else if (p.final_state && on && (MODE == kScanSlots || w.seg == p.nseg - 1)) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) st_state(p.final_state + (w.b * p.C + c + k) * p.N + 4 * g, h[k]);
+    st_states_wide<S>(p.final_state + state_at, p.N, h, swap);
   }
 }
 
 // One token per slot: a stream of the states. The lanes of a channel pair
 // each work the token's step size out for themselves.
 constexpr int kDecodeThreads = 128;
-template <class E, int LPC>
+template <class E, int LPC, int S>
 __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanParams p) {
   const int64_t i = (int64_t)blockIdx.x * kDecodeThreads + threadIdx.x;
   const int64_t np = p.C / 2, all = p.B * np * LPC;
   const int g = (int)(i % LPC);
   const int64_t k0 = min(i, all - 1) / LPC, s = k0 / np, c = (k0 - s * np) * 2;
-  const bool on = i < all && 4 * g < p.N;
+  const bool on = i < all && S * g < p.N;
   const int64_t grp = c / p.Cg;
   const float2 x = ld_pair(static_cast<const E*>(p.x) + s * p.C + c);
   const float2 dt = ld_pair(static_cast<const E*>(p.dt) + s * p.C + c);
   const float2 z = p.z ? ld_pair(static_cast<const E*>(p.z) + s * p.C + c) : splat2(0.f);
   const float2 bias = p.dt_bias ? ld_pair(p.dt_bias + c) : splat2(0.f);
   const float2 D = p.D ? ld_pair(p.D + c) : splat2(0.f);
-  float Bf[4] = {0.f, 0.f, 0.f, 0.f}, Cf[4] = {0.f, 0.f, 0.f, 0.f};
+  float Bf[S] = {}, Cf[S] = {};
   if (on) {
-    Pack<E, 4> pb, pc;
-    pb.load(static_cast<const E*>(p.Bm) + (s * p.G + grp) * p.N + 4 * g);
-    pc.load(static_cast<const E*>(p.Cm) + (s * p.G + grp) * p.N + 4 * g);
+    Pack<E, S> pb, pc;
+    pb.load(static_cast<const E*>(p.Bm) + (s * p.G + grp) * p.N + S * g);
+    pc.load(static_cast<const E*>(p.Cm) + (s * p.G + grp) * p.N + S * g);
     pb.get(Bf);
     pc.get(Cf);
   }
-  const State4 Bv = {{make_float2(Bf[0], Bf[1]), make_float2(Bf[2], Bf[3])}};
-  const State4 Cv = {{make_float2(Cf[0], Cf[1]), make_float2(Cf[2], Cf[3])}};
-  float out[2];
+  float* st = p.final_state + (s * p.C + c) * p.N + S * g;
+  States<S> h = ld_states_wide<S>(st, p.N, on);
+  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, on), kLog2e);
+  const float2 d = scan_step_size2(dt, bias, p.softplus);
+  Row<S> Bv, Cv;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float* st = p.final_state + (s * p.C + c + k) * p.N + 4 * g;
-    State4 h = ld_state(st, on);
-    const State4 A2 = scale4(ld_state(p.A + (c + k) * p.N + 4 * g, on), kLog2e);
-    const float d = scan_step_size(k ? dt.y : dt.x, k ? bias.y : bias.x, p.softplus);
-    scan_absorb(h, scan_decay(d, A2), __fmul_rn(d, k ? x.y : x.x), Bv);
-    out[k] = scan_dot(h, Cv);
-    if (on) st_state(st, h);
-  }
+  for (int n = 0; n < S; ++n) Bv.n[n] = Bf[n], Cv.n[n] = Cf[n];
+  scan_absorb(h, scan_decay(d, A2), mul2(d, x), Bv);
+  if (on) st_states_wide<S>(st, p.N, h, 0);
+  const float2 dot = scan_dot<S>(h, Cv);
+  float out[2] = {dot.x, dot.y};
   // one lane bit at a time, as the walk's halving steps do
 #pragma unroll
   for (int m = 1; m < LPC; m *= 2) {
@@ -259,10 +220,9 @@ __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanP
     out[1] = __fadd_rn(out[1], __shfl_xor_sync(0xffffffffu, out[1], m));
   }
   if (i < all && g == 0) {
-    const float g0 = p.z ? __fmul_rn(z.x, sigmoid_f(z.x)) : 1.f, g1 = p.z ? __fmul_rn(z.y, sigmoid_f(z.y)) : 1.f;
-    const float2 y = make_float2(__fmul_rn(__fadd_rn(out[0], __fmul_rn(D.x, x.x)), g0),
-                                 __fmul_rn(__fadd_rn(out[1], __fmul_rn(D.y, x.y)), g1));
-    st_pair(static_cast<E*>(p.y) + s * p.C + c, y);
+    const float2 gate = p.z ? mul2(z, sigmoid2(z)) : splat2(1.f), e = mul2(D, x);
+    st_pair(static_cast<E*>(p.y) + s * p.C + c,
+            make_float2(__fmul_rn(__fadd_rn(out[0], e.x), gate.x), __fmul_rn(__fadd_rn(out[1], e.y), gate.y)));
   }
 }
 
@@ -272,51 +232,61 @@ wkv_status launched(const char* what, const char** why) {
   return WKV_ERR_CUDA;
 }
 
-template <class E, int LPC, int MODE>
+template <class E, int LPC, int S, int MODE>
 wkv_status run_walk(const ScanParams& p, cudaStream_t st, const char** why) {
-  using Geo = ScanGeom<E, LPC>;
-  constexpr size_t smem = 2 * sizeof(ScanBuf<Geo::CB, Geo::NP>);
+  using Geo = ScanGeom<E, LPC, S>;
+  constexpr size_t smem = sizeof(ScanFwdShared<E, Geo>);
+  static_assert(smem <= 227 * 1024, "the tiles fit an SM");
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(scan_fwd_kernel<E, LPC, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaFuncSetAttribute(scan_fwd_kernel<E, LPC, S, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess) {
     *why = "scan kernel: shared memory request failed";
     return WKV_ERR_CUDA;
   }
   const int64_t grid = p.B * p.nseg * p.G * p.nbg;
-  scan_fwd_kernel<E, LPC, MODE><<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
+  scan_fwd_kernel<E, LPC, S, MODE><<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
   return launched("scan kernel launch failed", why);
 }
 
-template <class E, int LPC>
+template <class E, int LPC, int S>
 wkv_status run_forward(const ScanArgs& a, cudaStream_t st, const char** why) {
   const ScanCut cut = scan_fwd_cut(a.B, a.T, a.C, a.N, a.G);
   const ScanParams p = scan_params(a, cut);
   if (cut.nseg > 1)
-    if (wkv_status s = run_walk<E, LPC, kScanCarry>(p, st, why)) return s;
-  return run_walk<E, LPC, kScanMain>(p, st, why);
+    if (wkv_status s = run_walk<E, LPC, S, kScanCarry>(p, st, why)) return s;
+  return run_walk<E, LPC, S, kScanMain>(p, st, why);
 }
-template <class E, int LPC>
+template <class E, int LPC, int S>
 wkv_status run_slots(const ScanArgs& a, cudaStream_t st, unsigned* err, const char** why) {
   ScanParams p = scan_params(a, ScanCut{1, 0});
   p.err = err;
-  return run_walk<E, LPC, kScanSlots>(p, st, why);
+  return run_walk<E, LPC, S, kScanSlots>(p, st, why);
 }
-template <class E, int LPC>
+template <class E, int LPC, int S>
 wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
   const ScanParams p = scan_params(a, ScanCut{1, 0});
-  const int64_t threads = a.B * (a.C / 2) * LPC;
-  scan_decode_kernel<E, LPC><<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
+  constexpr int DL = LPC * S / 4;  // a stream of states: 16 bytes per lane and channel
+  const int64_t threads = a.B * (a.C / 2) * DL;
+  scan_decode_kernel<E, DL, 4><<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
   return launched("scan decode kernel launch failed", why);
 }
 
-#define WKV_SCAN_DISPATCH(CALL)                                           \
-  const bool bf = a.dtype == WKV_BF16;                                    \
-  switch (scan_lanes(a.N)) {                                              \
-    case 2: return bf ? CALL(__nv_bfloat16, 2) : CALL(float, 2);          \
-    case 4: return bf ? CALL(__nv_bfloat16, 4) : CALL(float, 4);          \
-    case 8: return bf ? CALL(__nv_bfloat16, 8) : CALL(float, 8);          \
-    default: return bf ? CALL(__nv_bfloat16, 16) : CALL(float, 16);       \
+// Lanes and states per lane by state size. Two states per lane up to 16: with
+// four (half the lanes) a launch has half the warps, and what it saves in
+// lane exchanges it loses in waiting: 411 against 380 us at B=8 T=2048 C=2560
+// N=16, the same where there are channels enough.
+#ifdef WKV_QUICK
+#define WKV_SCAN_DISPATCH(CALL) return CALL(__nv_bfloat16, 8, 2);
+#else
+#define WKV_SCAN_DISPATCH(CALL)                                                   \
+  const bool bf = a.dtype == WKV_BF16;                                            \
+  switch (scan_padded_states(a.N)) {                                              \
+    case 8: return bf ? CALL(__nv_bfloat16, 4, 2) : CALL(float, 4, 2);            \
+    case 16: return bf ? CALL(__nv_bfloat16, 8, 2) : CALL(float, 8, 2);           \
+    case 32: return bf ? CALL(__nv_bfloat16, 8, 4) : CALL(float, 8, 4);           \
+    default: return bf ? CALL(__nv_bfloat16, 16, 4) : CALL(float, 16, 4);         \
   }
+#endif
 
 // Pieces along T: none where the channels alone give two CTAs per SM, since
 // the carry pass costs most of a second walk; else about four CTAs per SM,
@@ -339,17 +309,17 @@ ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
 }
 
 wkv_status launch_scan_forward(const ScanArgs& a, cudaStream_t stream, const char** why) {
-#define CALL(E, L) (run_forward<E, L>(a, stream, why))
+#define CALL(E, L, S) (run_forward<E, L, S>(a, stream, why))
   WKV_SCAN_DISPATCH(CALL)
 #undef CALL
 }
 wkv_status launch_scan_chunk_step(const ScanArgs& a, cudaStream_t stream, unsigned* err, const char** why) {
-#define CALL(E, L) (run_slots<E, L>(a, stream, err, why))
+#define CALL(E, L, S) (run_slots<E, L, S>(a, stream, err, why))
   WKV_SCAN_DISPATCH(CALL)
 #undef CALL
 }
 wkv_status launch_scan_decode_step(const ScanArgs& a, cudaStream_t stream, const char** why) {
-#define CALL(E, L) (run_decode<E, L>(a, stream, why))
+#define CALL(E, L, S) (run_decode<E, L, S>(a, stream, why))
   WKV_SCAN_DISPATCH(CALL)
 #undef CALL
 }
