@@ -20,46 +20,46 @@ namespace wkv {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvU = 4;     // tokens whose loads are issued together
-constexpr int kConvBwdN = 4;  // channels per thread of the backward
-
+constexpr int kConvU = 4;      // tokens whose loads are issued together, one batch ahead (forward)
+constexpr int kConvBwdU = 4;  // (backward)
+constexpr int kConvBwdN = 4;        // channels per thread of the backward
 template <class E>
 constexpr int kConvN = 16 / (int)sizeof(E);  // channels per thread elsewhere
 
 // pre of one token: win[0 .. W-2] the tokens before it (oldest first), cur the token.
 template <int W, int N>
-__device__ __forceinline__ void conv_pre(const float (&w)[W][N], const float (&bias)[N], const float (&win)[W - 1][N],
-                                         const float (&cur)[N], float (&pre)[N]) {
+__device__ __forceinline__ void conv_pre(const float2 (&w)[W][N / 2], const float2 (&bias)[N / 2],
+                                         const float2 (&win)[W - 1][N / 2], const float2 (&cur)[N / 2],
+                                         float2 (&pre)[N / 2]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float s = bias[n];
+  for (int n = 0; n < N / 2; ++n) {
+    float2 s = bias[n];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s = __fmaf_rn(w[j][n], win[j][n], s);
-    pre[n] = __fmaf_rn(w[W - 1][n], cur[n], s);
+    for (int j = 0; j < W - 1; ++j) s = fma2(w[j][n], win[j][n], s);
+    pre[n] = fma2(w[W - 1][n], cur[n], s);
   }
 }
 template <int W, int N>
-__device__ __forceinline__ void conv_shift(float (&win)[W - 1][N], const float (&cur)[N]) {
+__device__ __forceinline__ void conv_shift(float2 (&win)[W - 1][N / 2], const float2 (&cur)[N / 2]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < N / 2; ++n) {
 #pragma unroll
     for (int j = 0; j + 1 < W - 1; ++j) win[j][n] = win[j + 1][n];
     win[W - 2][n] = cur[n];
   }
 }
-template <class E, int W, int N>
-__device__ __forceinline__ void conv_store(E* y, const float (&pre)[N], bool silu) {
-  float o[N];
+template <class E, int W, int N, bool SILU>
+__device__ __forceinline__ void conv_store(E* y, const float2 (&pre)[N / 2]) {
+  float2 o[N / 2];
 #pragma unroll
-  for (int n = 0; n < N; ++n) o[n] = silu ? __fmul_rn(pre[n], sigmoid_f(pre[n])) : pre[n];
-  Pack<E, N> p;
-  p.set(o);
-  p.store(y);
+  for (int n = 0; n < N / 2; ++n) o[n] = SILU ? mul2(pre[n], sigmoid2(pre[n])) : pre[n];
+  set2<E, N>(o).store(y);
 }
 // The W-1 tokens before token t0 of a sequence whose first token is at x and
 // whose earlier ones are at prev (null: zeros).
 template <class E, int W, int N>
-__device__ __forceinline__ void conv_window(const E* x, const E* prev, int64_t t0, int64_t C, float (&win)[W - 1][N]) {
+__device__ __forceinline__ void conv_window(const E* x, const E* prev, int64_t t0, int64_t C,
+                                            float2 (&win)[W - 1][N / 2]) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int64_t t = t0 - (W - 1) + j;
@@ -69,20 +69,20 @@ __device__ __forceinline__ void conv_window(const E* x, const E* prev, int64_t t
       p.load(x + t * C);
     else if (prev)
       p.load(prev + (t + W - 1) * C);
-    p.get(win[j]);
+    get2(p, win[j]);
   }
 }
 
 // SLOTS: sequence b is slot b, tokens cu[b] .. cu[b+1] of the packed tensors,
 // and x_prev is the slots' state; its tokens are split over the nrun CTAs.
-template <class E, int W, bool SLOTS>
+template <class E, int W, bool SILU, bool SLOTS>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restrict__ x, const float* __restrict__ weight,
                                                                 const float* __restrict__ bias,
                                                                 const E* __restrict__ x_prev, E* __restrict__ y, int64_t T,
-                                                                int64_t C, int ncb, int nrun, int64_t Lt, int silu,
+                                                                int64_t C, int ncb, int nrun, int64_t Lt,
                                                                 const int32_t* __restrict__ cu, int64_t n_tokens,
                                                                 unsigned* err) {
-  constexpr int N = kConvN<E>;
+  constexpr int N = kConvN<E>, U = kConvU;
   const int cb = (int)(blockIdx.x % ncb);
   const int rest = (int)(blockIdx.x / ncb);
   const int run = rest % nrun;
@@ -101,33 +101,42 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restr
     T = end - beg;
     Lt = (T + nrun - 1) / nrun;
   }
-  const int64_t t0 = run * Lt, t1 = t0 + Lt < T ? t0 + Lt : T;
-  if (t0 >= t1) return;
-  float w[W][N], bi[N], win[W - 1][N];
-#pragma unroll
-  for (int j = 0; j < W; ++j) ld_param<N>(weight + (int64_t)j * C + c, w[j], 0.f);
-  ld_param<N>(bias ? bias + c : nullptr, bi, 0.f);
+  const int64_t t0 = run * Lt;
+  if (t0 >= T) return;
+  int left = (int)min(Lt, T - t0);  // tokens of the run still to load
   const E* xs = x + first * C + c;
-  conv_window<E, W, N>(xs, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
   const E* xp = xs + t0 * C;
   E* yp = y + (first + t0) * C + c;
-  for (int64_t t = t0; t < t1; t += kConvU) {
-    Pack<E, N> raw[kConvU];
+  Pack<E, N> raw[U];
 #pragma unroll
-    for (int j = 0; j < kConvU; ++j)
-      if (t + j < t1) raw[j].load(xp + j * C);
+  for (int j = 0; j < U; ++j)
+    if (j < left) raw[j].load(xp + j * C);
+  float2 w[W][N / 2], bi[N / 2], win[W - 1][N / 2];
 #pragma unroll
-    for (int j = 0; j < kConvU; ++j) {
-      if (t + j < t1) {
-        float cur[N], pre[N];
-        raw[j].get(cur);
+  for (int j = 0; j < W; ++j) ld_param2<N>(weight + (int64_t)j * C + c, w[j], 0.f);
+  ld_param2<N>(bias ? bias + c : nullptr, bi, 0.f);
+  conv_window<E, W, N>(xs, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
+  while (true) {
+    Pack<E, N> next[U];
+    xp += U * C;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (U + j < left) next[j].load(xp + j * C);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (j < left) {
+        float2 cur[N / 2], pre[N / 2];
+        get2(raw[j], cur);
         conv_pre<W, N>(w, bi, win, cur, pre);
-        conv_store<E, W, N>(yp + j * C, pre, silu);
+        conv_store<E, W, N, SILU>(yp + j * C, pre);
         conv_shift<W, N>(win, cur);
       }
     }
-    xp += kConvU * C;
-    yp += kConvU * C;
+    left -= U;
+    if (left <= 0) break;
+    yp += U * C;
+#pragma unroll
+    for (int j = 0; j < U; ++j) raw[j] = next[j];
   }
 }
 
@@ -173,114 +182,149 @@ __global__ void __launch_bounds__(kConvThreads) conv_decode_kernel(const E* __re
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j].load(st + j * C);
   rows[W - 1].load(x + b * C + c);
-  float w[W][N], bi[N], win[W - 1][N], cur[N], pre[N];
+  float2 w[W][N / 2], bi[N / 2], win[W - 1][N / 2], cur[N / 2], pre[N / 2];
 #pragma unroll
-  for (int j = 0; j < W; ++j) ld_param<N>(weight + (int64_t)j * C + c, w[j], 0.f);
-  ld_param<N>(bias ? bias + c : nullptr, bi, 0.f);
+  for (int j = 0; j < W; ++j) ld_param2<N>(weight + (int64_t)j * C + c, w[j], 0.f);
+  ld_param2<N>(bias ? bias + c : nullptr, bi, 0.f);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) rows[j].get(win[j]);
-  rows[W - 1].get(cur);
+  for (int j = 0; j < W - 1; ++j) get2(rows[j], win[j]);
+  get2(rows[W - 1], cur);
   conv_pre<W, N>(w, bi, win, cur, pre);
-  conv_store<E, W, N>(y + b * C + c, pre, silu);
+  if (silu)
+    conv_store<E, W, N, true>(y + b * C + c, pre);
+  else
+    conv_store<E, W, N, false>(y + b * C + c, pre);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j + 1].store(st + j * C);
 }
 
 // part: [W + 1][B * nrun][C] partial sums (gw_0 .. gw_{W-1}, gbias).
-template <class E, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const E* __restrict__ x, const float* __restrict__ weight,
+template <class E, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(const E* __restrict__ x, const float* __restrict__ weight,
                                                                 const float* __restrict__ bias,
                                                                 const E* __restrict__ x_prev, const E* __restrict__ gy,
                                                                 E* __restrict__ gx, E* __restrict__ gx_prev,
                                                                 float* __restrict__ part, int64_t B, int64_t T, int64_t C,
-                                                                int ncb, int nrun, int64_t Lt, int silu) {
-  constexpr int N = kConvBwdN;
+                                                                int ncb, int nrun, int64_t Lt) {
+  constexpr int N = kConvBwdN, H = N / 2, U = kConvBwdU;
   const int cb = (int)(blockIdx.x % ncb);
   const int rest = (int)(blockIdx.x / ncb);
   const int run = rest % nrun;
   const int64_t b = rest / nrun;
   const int64_t c = ((int64_t)cb * kConvThreads + threadIdx.x) * N;
   if (c >= C) return;
-  const int64_t t0 = run * Lt, t1 = t0 + Lt < T ? t0 + Lt : T;
-  float w[W][N], bi[N], win[W - 1][N];
+  const int64_t t0 = run * Lt, row = (b * T + t0) * C + c;
+  const int n = (int)min(Lt, T - t0);        // tokens of the run
+  const int there = (int)min(T - t0, (int64_t)n + W - 1);  // tokens to read: W-1 more complete gx
+  const E* xp = x + row;
+  const E* gp = gy + row;
+  // One batch of loads ahead.
+  Pack<E, N> xr[U], gr[U];
+  auto fetch = [&](int t, Pack<E, N>(&xo)[U], Pack<E, N>(&go)[U]) {
+    if (t + U <= there) {
 #pragma unroll
-  for (int j = 0; j < W; ++j) ld_param<N>(weight + (int64_t)j * C + c, w[j], 0.f);
-  ld_param<N>(bias ? bias + c : nullptr, bi, 0.f);
-  const int64_t row = b * T * C + c;
-  conv_window<E, W, N>(x + row, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
-  float gwin[W - 1][N], gw[W][N], gb[N];
+      for (int j = 0; j < U; ++j) {
+        xo[j].load(xp + j * C);
+        go[j].load(gp + j * C);
+      }
+    } else {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    gb[n] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) gwin[j][n] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) gw[j][n] = 0.f;
-  }
-  const int64_t stop = t1 + W - 1;  // the last W-1 steps only complete gx
-  for (int64_t t = t0; t < stop; t += kConvU) {
-    Pack<E, N> xr[kConvU], gr[kConvU];
-#pragma unroll
-    for (int j = 0; j < kConvU; ++j) {
-      xr[j].zero();
-      gr[j].zero();
-      if (t + j < stop && t + j < T) {
-        xr[j].load(x + row + (t + j) * C);
-        gr[j].load(gy + row + (t + j) * C);
+      for (int j = 0; j < U; ++j) {
+        xo[j].zero();
+        go[j].zero();
+        if (t + j < there) {
+          xo[j].load(xp + j * C);
+          go[j].load(gp + j * C);
+        }
       }
     }
+    xp += U * C;
+    gp += U * C;
+  };
+  fetch(0, xr, gr);
+  float2 w[W][H], bi[H], win[W - 1][H];
 #pragma unroll
-    for (int j = 0; j < kConvU; ++j) {
-      if (t + j < stop) {
-        float cur[N], g[N], pre[N], o[N];
-        xr[j].get(cur);
-        gr[j].get(g);
+  for (int j = 0; j < W; ++j) ld_param2<N>(weight + (int64_t)j * C + c, w[j], 0.f);
+  ld_param2<N>(bias ? bias + c : nullptr, bi, 0.f);
+  conv_window<E, W, N>(x + b * T * C + c, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
+  float2 gwin[W - 1][H], gw[W][H], gb[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    gb[i] = splat2(0.f);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) gwin[j][i] = splat2(0.f);
+#pragma unroll
+    for (int j = 0; j < W; ++j) gw[j][i] = splat2(0.f);
+  }
+  E* op = gx + row - (W - 1) * C;  // gx of token t - (W-1)
+  // One batch from token t. EDGE: some of its tokens are not the run's own, or
+  // complete a gx that is not.
+  auto batch = [&](auto edge, int t) {
+    constexpr bool EDGE = decltype(edge)::value;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (!EDGE || t + j < n + W - 1) {
+        float2 cur[H], g[H], pre[H], o[H];
+        get2(xr[j], cur);
+        get2(gr[j], g);
         conv_pre<W, N>(w, bi, win, cur, pre);
-        const bool mine = t + j < t1, past = t + j >= T;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (silu) {
+        for (int i = 0; i < H; ++i) {
+          if constexpr (SILU) {
             // d silu = p (1 + pre (1 - p)), p = sigmoid(pre)
-            const float p = sigmoid_f(pre[n]);
-            g[n] = __fmul_rn(g[n], __fmul_rn(p, __fmaf_rn(pre[n], __fsub_rn(1.f, p), 1.f)));
+            const float2 p = sigmoid2(pre[i]);
+            g[i] = mul2(g[i], mul2(p, fma2(pre[i], sub2(splat2(1.f), p), splat2(1.f))));
           }
-          if (mine) {
+          if (EDGE && t + j >= there) g[i] = splat2(0.f);  // whatever the window holds
+          if (!EDGE || t + j < n) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) gw[i][n] = __fmaf_rn(g[n], win[i][n], gw[i][n]);
-            gw[W - 1][n] = __fmaf_rn(g[n], cur[n], gw[W - 1][n]);
-            gb[n] = __fadd_rn(gb[n], g[n]);
+            for (int k = 0; k < W - 1; ++k) gw[k][i] = fma2(g[i], win[k][i], gw[k][i]);
+            gw[W - 1][i] = fma2(g[i], cur[i], gw[W - 1][i]);
+            gb[i] = add2(gb[i], g[i]);
           }
-          if (past) g[n] = 0.f;  // whatever the window holds
-          // gx_{t-W+1} = sum_i w_i gpre_{t-i}
-          float s = __fmul_rn(w[0][n], g[n]);
+          // gx_{t-W+1} = sum_k w_k gpre_{t-k}
+          float2 s = mul2(w[0][i], g[i]);
 #pragma unroll
-          for (int i = 1; i < W; ++i) s = __fmaf_rn(w[i][n], gwin[W - 1 - i][n], s);
-          o[n] = s;
+          for (int k = 1; k < W; ++k) s = fma2(w[k][i], gwin[W - 1 - k][i], s);
+          o[i] = s;
         }
-        const int64_t to = t + j - (W - 1);
-        Pack<E, N> q;
-        q.set(o);
-        if (to >= t0)
-          q.store(gx + row + to * C);
+        const int to = t + j - (W - 1);  // in the run
+        if (!EDGE || to >= 0)
+          set2<E, N>(o).store(op + j * C);
         else if (t0 == 0 && gx_prev)
-          q.store(gx_prev + (b * (W - 1) + to + W - 1) * C + c);
+          set2<E, N>(o).store(gx_prev + (b * (W - 1) + to + W - 1) * C + c);
         conv_shift<W, N>(win, cur);
         conv_shift<W, N>(gwin, g);
       }
     }
+  };
+  for (int t = 0; t < n + W - 1; t += U) {
+    Pack<E, N> xn[U], gn[U];
+    fetch(t + U, xn, gn);
+    if (t >= W - 1 && t + U <= n)
+      batch(BoolConst<false>{}, t);
+    else
+      batch(BoolConst<true>{}, t);
+    op += U * C;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      xr[j] = xn[j];
+      gr[j] = gn[j];
+    }
   }
   const int64_t rows = B * nrun, prow = b * nrun + run;
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-    *reinterpret_cast<float4*>(part + (j * rows + prow) * C + c) = make_float4(gw[j][0], gw[j][1], gw[j][2], gw[j][3]);
-  *reinterpret_cast<float4*>(part + (W * rows + prow) * C + c) = make_float4(gb[0], gb[1], gb[2], gb[3]);
+  for (int j = 0; j <= W; ++j) {
+    const float2(&v)[H] = j < W ? gw[j < W ? j : 0] : gb;
+    set2<float, N>(v).store(part + (j * rows + prow) * C + c);
+  }
 }
 
-ConvShape conv_shape(int64_t B, int64_t T, int64_t C, int vec, int min_run) {
+ConvShape conv_shape(int64_t B, int64_t T, int64_t C, int vec, int min_run, int ctas) {
   ConvShape s;
   s.ncb = (int)ceil_div(C, (int64_t)kConvThreads * vec);
-  // runs per sequence: enough CTAs for ~16 per SM, runs of at least min_run tokens
-  const int64_t want = ceil_div(148 * 16, std::max<int64_t>(1, B * s.ncb));
+  // runs per sequence: enough for that many CTAs per SM, of at least min_run tokens
+  const int64_t want = ceil_div(148 * ctas, std::max<int64_t>(1, B * s.ncb));
   const int64_t most = std::max<int64_t>(1, ceil_div(T, min_run));
   const int64_t nrun = std::max<int64_t>(1, std::min(want, most));
   s.Lt = (int)std::max<int64_t>(1, ceil_div(T, nrun));
@@ -296,19 +340,21 @@ wkv_status launched(const char* what, const char** why) {
 
 template <class E, int W>
 wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
-  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, 16);
-  conv_fwd_kernel<E, W, false><<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
+  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, 16, 16);
+  const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, false> : conv_fwd_kernel<E, W, false, false>;
+  kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), static_cast<E*>(a.y), a.T, a.C, s.ncb,
-      s.nrun, s.Lt, a.silu, nullptr, 0, nullptr);
+      s.nrun, s.Lt, nullptr, 0, nullptr);
   return launched("conv forward kernel launch failed", why);
 }
 template <class E, int W>
 wkv_status run_chunk(const ConvArgs& a, cudaStream_t st, unsigned* err, const char** why) {
   // the lengths are on the device: the runs are cut for the mean length
-  const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, 16);
-  conv_fwd_kernel<E, W, true><<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
+  const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, 16, 16);
+  const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, true> : conv_fwd_kernel<E, W, false, true>;
+  kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.state), static_cast<E*>(a.y), 0, a.C, s.ncb,
-      s.nrun, 0, a.silu, a.cu, a.n_tokens, err);
+      s.nrun, 0, a.cu, a.n_tokens, err);
   if (wkv_status e = launched("conv chunk step kernel launch failed", why)) return e;
   conv_state_kernel<E, W><<<(unsigned)ceil_div(a.B * (a.C / kConvN<E>), kConvThreads), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), static_cast<E*>(a.state), a.B, a.C, a.cu, a.n_tokens);
@@ -323,13 +369,15 @@ wkv_status run_decode(const ConvArgs& a, cudaStream_t st, const char** why) {
 template <class E, int W>
 wkv_status run_bwd(const ConvArgs& a, cudaStream_t st, const char** why) {
   const ConvShape s = conv_bwd_shape(a.B, a.T, a.C);
-  conv_bwd_kernel<E, W><<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
+  const auto kernel = a.silu ? conv_bwd_kernel<E, W, true> : conv_bwd_kernel<E, W, false>;
+  kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), static_cast<const E*>(a.gy),
-      static_cast<E*>(a.gx), static_cast<E*>(a.gx_prev), a.part, a.B, a.T, a.C, s.ncb, s.nrun, s.Lt, a.silu);
+      static_cast<E*>(a.gx), static_cast<E*>(a.gx_prev), a.part, a.B, a.T, a.C, s.ncb, s.nrun, s.Lt);
   if (wkv_status e = launched("conv backward kernel launch failed", why)) return e;
-  const int64_t rows = a.B * s.nrun;
-  if (wkv_status e = launch_sum_rows(a.part, W, rows, a.C, a.gweight, st, why)) return e;
-  return a.gbias ? launch_sum_rows(a.part + W * rows * a.C, 1, rows, a.C, a.gbias, st, why) : WKV_OK;
+  SumOutputs out{};
+  for (int j = 0; j < W; ++j) out.plane[j] = a.gweight + j * a.C;
+  out.plane[W] = a.gbias;
+  return launch_sum_rows(a.part, W + 1, a.B * s.nrun, a.C, out, st, why);
 }
 
 #define WKV_CONV_DISPATCH(CALL)                                                        \
@@ -342,7 +390,7 @@ wkv_status run_bwd(const ConvArgs& a, cudaStream_t st, const char** why) {
 
 }  // namespace
 
-ConvShape conv_bwd_shape(int64_t B, int64_t T, int64_t C) { return conv_shape(B, T, C, kConvBwdN, 32); }
+ConvShape conv_bwd_shape(int64_t B, int64_t T, int64_t C) { return conv_shape(B, T, C, kConvBwdN, 32, 16); }
 
 wkv_status launch_conv_forward(const ConvArgs& a, cudaStream_t stream, const char** why) {
 #define CALL(E, W) (run_fwd<E, W>(a, stream, why))

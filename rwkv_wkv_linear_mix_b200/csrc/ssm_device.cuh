@@ -70,21 +70,42 @@ struct Pack {
   }
 };
 
-// N float32 parameters (16-byte aligned), or a constant where there are none.
+// The same as packed pairs.
+template <class E, int N>
+__device__ __forceinline__ void get2(const Pack<E, N>& p, float2 (&f)[N / 2]) {
+  float v[N];
+  p.get(v);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+template <class E, int N>
+__device__ __forceinline__ Pack<E, N> set2(const float2 (&f)[N / 2]) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[2 * i] = f[i].x, v[2 * i + 1] = f[i].y;
+  Pack<E, N> p;
+  p.set(v);
+  return p;
+}
+
+// N float32 parameters, or a constant where there are none.
 template <int N>
 __device__ __forceinline__ void ld_param(const float* p, float (&f)[N], float otherwise) {
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = otherwise;
   if (p) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p + i);
-      f[i] = q.x;
-      f[i + 1] = q.y;
-      f[i + 2] = q.z;
-      f[i + 3] = q.w;
-    }
+    Pack<float, N> q;
+    q.load(p);
+    q.get(f);
   }
+}
+
+template <int N>
+__device__ __forceinline__ void ld_param2(const float* p, float2 (&f)[N / 2], float otherwise) {
+  float v[N];
+  ld_param<N>(p, v, otherwise);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
 
 // sigmoid(x) = 1 / (1 + e^-x). e^-x overflows to inf below -88, whose
@@ -107,6 +128,22 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
   p = fma2(p, q, splat2(1.f));
   return fma2(add2(s, s), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
+
+// One copy of 8 or 16 bytes to shared memory that the thread does not wait
+// for; zeros where there is nothing to copy (src is then not read).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
+  static_assert(BYTES == 8 || BYTES == 16, "copy sizes");
+  const int n = there ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most LEFT of the thread's groups of copies are in flight.
+template <int LEFT = 0>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Sums of NV values over the NL lanes that differ in the lane bits
 // BIT .. BIT * NL / 2, in halving steps: each step sends half of the values

@@ -10,9 +10,14 @@ namespace wkv {
 // Address of the current device's error word (capi.cu).
 wkv_status device_error_word(unsigned** out);
 
-// out[i][c] = sum over the rows of part[i][rows][cols], in a fixed order.
-wkv_status launch_sum_rows(const float* part, int planes, int64_t rows, int64_t cols, float* out, cudaStream_t stream,
-                           const char** why);
+// out[i][c] = sum over the rows of part[i][rows][cols], in a fixed order, for
+// each plane i that has an output.
+struct SumOutputs {
+  static constexpr int kMost = 5;
+  float* plane[kMost];
+};
+wkv_status launch_sum_rows(const float* part, int planes, int64_t rows, int64_t cols, const SumOutputs& out,
+                           cudaStream_t stream, const char** why);
 
 // ---- short causal convolution ------------------------------------------------
 struct ConvArgs {

@@ -6,12 +6,13 @@
 //     gx = r (gn w - x r^2 mean(gn w x))
 //
 // A stream of short rows (token, head): 8 elements per lane, K / 8 lanes
-// (rounded up to a power of two) per row, sums by lane exchange. The rows of
-// kNormTokens tokens or so go to one CTA, which first works the tokens'
-// sines and cosines out once for all their heads: angles p * f reach 2^31
-// turns, so they are reduced to half a turn in float64 and only then
-// evaluated in float32. Halves of a pair i, i + R/2 lie in lanes R/16 apart
-// and are exchanged by shuffle.
+// (rounded up to a power of two) per row, sums by lane exchange. A group of
+// lanes keeps its token and walks over heads, the loads of several heads in
+// flight, so that the token's sines and cosines stay in registers. They are
+// worked out once per token by the CTA: angles p * f reach 2^31 turns, so they
+// are reduced to half a turn in float64 and only then evaluated in float32.
+// Halves of a pair i, i + R/2 lie in lanes R/16 apart and are exchanged by
+// shuffle.
 #include "ssm_device.cuh"
 
 namespace wkv {
@@ -19,21 +20,25 @@ namespace wkv {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormV = 8;         // elements per lane
-constexpr int kNormMaxTokens = 16;  // tokens per CTA, at most
+constexpr int kNormV = 8;  // elements per lane
+constexpr int kNormU = 4;     // heads whose loads are issued together (forward)
+constexpr int kNormBwdU = 4; // (backward)
 
 struct NormRows {
   int64_t tokens, T;
-  int Hq, Hk, K, R, tok_cta;  // tok_cta: tokens per CTA and step
+  int Hq, Hk, K, R;
+  int gpt;  // groups of lanes per token (a power of two)
   float eps, inv_K;
   const float* inv_freq;
   const int32_t* positions;
   int64_t pos_offset;
 };
+// Floats of a token's row of cosines (or sines), kept 16-byte aligned.
+__host__ __device__ __forceinline__ int norm_row(int R) { return (R / 2 + 3) & ~3; }
 
-// cos and sin of the tokens [t0, t0 + n) into [t][R/2] tables.
+// cos and sin of the tokens [t0, t0 + n) into tables of rows.
 __device__ __forceinline__ void norm_angles(const NormRows& a, int64_t t0, int n, float* cs, float* sn) {
-  const int half = a.R / 2;
+  const int half = a.R / 2, row = norm_row(a.R);
   for (int i = threadIdx.x; i < n * half; i += kNormThreads) {
     const int t = i / half, f = i - t * half;
     const int64_t tok = t0 + t;
@@ -43,42 +48,63 @@ __device__ __forceinline__ void norm_angles(const NormRows& a, int64_t t0, int n
     turn -= rint(turn);
     float s, c;
     sincospif((float)(2.0 * turn), &s, &c);
-    cs[i] = c;
-    sn[i] = s;
+    cs[t * row + f] = c;
+    sn[t * row + f] = s;
   }
 }
 
-// Turns the 8 elements at e0 = 8 * l of a row (forward: by the angle; BACK:
-// by minus the angle). c, s: the token's tables.
-template <bool IL, bool BACK>
-__device__ __forceinline__ void norm_turn(float (&v)[kNormV], int l, int row_lane0, int R, const float* c, const float* s) {
-  const int e0 = l * kNormV;
-  if constexpr (IL) {
-#pragma unroll
-    for (int m = 0; m < kNormV / 2; ++m) {
-      if (e0 + 2 * m < R) {
-        const float cc = c[e0 / 2 + m], ss = BACK ? -s[e0 / 2 + m] : s[e0 / 2 + m];
-        const float a = v[2 * m], b = v[2 * m + 1];
-        v[2 * m] = __fmaf_rn(a, cc, -__fmul_rn(b, ss));
-        v[2 * m + 1] = __fmaf_rn(a, ss, __fmul_rn(b, cc));
-      }
-    }
-  } else {
+// What a lane needs to turn its 8 elements (entries 8 l .. of a head).
+template <bool IL>
+struct NormTurn {
+  static constexpr int NF = IL ? kNormV / 2 : kNormV;
+  float c[NF], s[NF];  // s: with the sign of the other half's term
+  int src;             // lane of the other half of the pairs
+  bool in;             // whether the lane's entries turn (interleaved: see R)
+  // cs, sn: the token's rows
+  __device__ __forceinline__ void load(const float* cs, const float* sn, int l, int row_lane0, int R) {
     const int lanes = R / (2 * kNormV);  // lanes that hold the first half
-    const bool lo = l < lanes, in = l < 2 * lanes;
-    const int src = row_lane0 + (lo ? l + lanes : in ? l - lanes : l);
-    const int f0 = (lo ? l : l - lanes) * kNormV;
+    const bool lo = l < lanes;
+    in = IL ? l * kNormV < R : l < 2 * lanes;
+    src = row_lane0 + (lo ? l + lanes : in ? l - lanes : l);
+    const int f0 = IL ? l * NF : (lo ? l : l - lanes) * kNormV;
 #pragma unroll
-    for (int i = 0; i < kNormV; ++i) {
-      const float other = __shfl_sync(0xffffffffu, v[i], src);
-      if (in) {
-        const float cc = c[f0 + i];
-        const float ss = (lo != BACK) ? -s[f0 + i] : s[f0 + i];
-        v[i] = __fmaf_rn(v[i], cc, __fmul_rn(other, ss));
+    for (int i = 0; i < NF; ++i) c[i] = 1.f, s[i] = 0.f;
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < NF; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(cs + f0 + i), b = *reinterpret_cast<const float4*>(sn + f0 + i);
+        c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
+        s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
+      }
+      if (IL) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+          if (l * kNormV + 2 * i >= R) c[i] = 1.f, s[i] = 0.f;
+      } else if (lo) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) s[i] = -s[i];
       }
     }
   }
-}
+  // By the angle, or (BACK) by minus the angle. All 32 lanes call it.
+  template <bool BACK>
+  __device__ __forceinline__ void turn(float (&v)[kNormV]) const {
+    if constexpr (IL) {
+#pragma unroll
+      for (int m = 0; m < NF; ++m) {
+        const float ss = BACK ? -s[m] : s[m], x = v[2 * m], y = v[2 * m + 1];
+        v[2 * m] = __fmaf_rn(x, c[m], -__fmul_rn(y, ss));
+        v[2 * m + 1] = __fmaf_rn(x, ss, __fmul_rn(y, c[m]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNormV; ++i) {
+        const float other = __shfl_sync(0xffffffffu, v[i], src);
+        v[i] = __fmaf_rn(v[i], c[i], __fmul_rn(other, BACK ? -s[i] : s[i]));
+      }
+    }
+  }
+};
 
 template <int LR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -87,129 +113,144 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The heads of one tensor for a group of lanes: hsub, hsub + gpt, ..; the
+// whole warp runs as many steps as any of its groups needs.
+template <class E, int LR, bool IL>
+__device__ __forceinline__ void norm_heads(const NormRows& a, const E* in, E* out, int H, int64_t tok, bool there, int hsub,
+                                           int l, const float* weight, const NormTurn<IL>& turn) {
+  const bool on = there && l * kNormV < a.K;
+  float w[kNormV];
+  ld_param<kNormV>(weight && on ? weight + l * kNormV : nullptr, w, 1.f);
+  const int64_t base = tok * H * a.K + l * kNormV;
+  for (int h0 = hsub, step = 0; step < H; step += kNormU * a.gpt, h0 += kNormU * a.gpt) {
+    Pack<E, kNormV> p[kNormU];
+#pragma unroll
+    for (int u = 0; u < kNormU; ++u) {
+      p[u].zero();
+      if (on && h0 + u * a.gpt < H) p[u].load(in + base + (int64_t)(h0 + u * a.gpt) * a.K);
+    }
+#pragma unroll
+    for (int u = 0; u < kNormU; ++u) {
+      if (step + u * a.gpt >= H) break;  // no group has such a head
+      float v[kNormV], ss = 0.f;
+      p[u].get(v);
+#pragma unroll
+      for (int i = 0; i < kNormV; ++i) ss = __fmaf_rn(v[i], v[i], ss);
+      const float rs = rsqrtf(__fmaf_rn(row_sum<LR>(ss), a.inv_K, a.eps));
+#pragma unroll
+      for (int i = 0; i < kNormV; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs), w[i]);
+      if (a.R) turn.template turn<false>(v);
+      if (on && h0 + u * a.gpt < H) {
+        p[u].set(v);
+        p[u].store(out + base + (int64_t)(h0 + u * a.gpt) * a.K);
+      }
+    }
+  }
+}
+
 // LR lanes per row.
 template <class E, int LR, bool IL>
 __global__ void __launch_bounds__(kNormThreads) norm_rotate_kernel(NormRows a, const E* q, const E* k,
                                                                    const float* __restrict__ wq,
                                                                    const float* __restrict__ wk, E* q_out, E* k_out) {
-  extern __shared__ float tab[];  // cos, then sin: [tok_cta][R/2]
-  const int64_t t0 = (int64_t)blockIdx.x * a.tok_cta;
-  const int nt = (int)min((int64_t)a.tok_cta, a.tokens - t0);
-  float* cs = tab;
-  float* sn = tab + a.tok_cta * (a.R / 2);
-  const int l = threadIdx.x % LR, row_lane0 = (threadIdx.x % 32) / LR * LR;
-  const bool on = l * kNormV < a.K;
-  float w[2][kNormV];
-  ld_param<kNormV>(wq && on ? wq + l * kNormV : nullptr, w[0], 1.f);
-  ld_param<kNormV>(wk && on ? wk + l * kNormV : nullptr, w[1], 1.f);
-  norm_angles(a, t0, nt, cs, sn);
-  __syncthreads();
-  const int H = a.Hq + a.Hk, rows = nt * H;
-  constexpr int RP = kNormThreads / LR;  // rows per pass
-  for (int r0 = 0; r0 < rows; r0 += RP) {  // whole warps stay: the rows' lanes exchange values
-    const int r = r0 + threadIdx.x / LR;
-    const bool have = r < rows && on;
-    const int t = r / H, h = r - t * H;
-    const bool key = h >= a.Hq;
-    const int64_t off = key ? ((t0 + t) * a.Hk + (h - a.Hq)) * (int64_t)a.K : ((t0 + t) * a.Hq + h) * (int64_t)a.K;
-    Pack<E, kNormV> p;
-    p.zero();
-    if (have) p.load((key ? k : q) + off + l * kNormV);
-    float v[kNormV];
-    p.get(v);
-    float ss = 0.f;
+  extern __shared__ float4 tab4[];
+  constexpr int RP = kNormThreads / LR;  // groups of lanes
+  const int ntok = RP / a.gpt, row = norm_row(a.R);
+  float* cs = reinterpret_cast<float*>(tab4);
+  float* sn = cs + ntok * row;
+  const int64_t t0 = (int64_t)blockIdx.x * ntok;
+  const int l = threadIdx.x % LR, grp = threadIdx.x / LR, t = grp / a.gpt, hsub = grp % a.gpt;
+  const int64_t left = a.tokens - t0;
+  NormTurn<IL> turn;
+  if (a.R) {
+    norm_angles(a, t0, (int)min((int64_t)ntok, left), cs, sn);
+    __syncthreads();
+    turn.load(cs + t * row, sn + t * row, l, (threadIdx.x % 32) / LR * LR, a.R);
+  }
+  norm_heads<E, LR, IL>(a, q, q_out, a.Hq, t0 + t, t < left, hsub, l, wq, turn);
+  norm_heads<E, LR, IL>(a, k, k_out, a.Hk, t0 + t, t < left, hsub, l, wk, turn);
+}
+
+// The same for the backward; gw: the lane's sums of the weight gradient.
+template <class E, int LR, bool IL>
+__device__ __forceinline__ void norm_heads_bwd(const NormRows& a, const E* in, const E* gout, E* gin, int H, int64_t tok,
+                                               bool there, int hsub, int l, const float (&w)[kNormV],
+                                               const NormTurn<IL>& turn, float (&gw)[kNormV]) {
+  const bool on = there && l * kNormV < a.K;
+  const int64_t base = tok * H * a.K + l * kNormV;
+  for (int h0 = hsub, step = 0; step < H; step += kNormBwdU * a.gpt, h0 += kNormBwdU * a.gpt) {
+    Pack<E, kNormV> px[kNormBwdU], pg[kNormBwdU];
 #pragma unroll
-    for (int i = 0; i < kNormV; ++i) ss = __fmaf_rn(v[i], v[i], ss);
-    ss = row_sum<LR>(ss);
-    const float rs = rsqrtf(__fmaf_rn(ss, a.inv_K, a.eps));
-#pragma unroll
-    for (int i = 0; i < kNormV; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rs), key ? w[1][i] : w[0][i]);
-    if (a.R) {
-      const int tt = min(t, nt - 1) * (a.R / 2);
-      norm_turn<IL, false>(v, l, row_lane0, a.R, cs + tt, sn + tt);
+    for (int u = 0; u < kNormBwdU; ++u) {
+      px[u].zero();
+      pg[u].zero();
+      if (on && h0 + u * a.gpt < H) {
+        px[u].load(in + base + (int64_t)(h0 + u * a.gpt) * a.K);
+        pg[u].load(gout + base + (int64_t)(h0 + u * a.gpt) * a.K);
+      }
     }
-    if (have) {
-      p.set(v);
-      p.store((key ? k_out : q_out) + off + l * kNormV);
+#pragma unroll
+    for (int u = 0; u < kNormBwdU; ++u) {
+      if (step + u * a.gpt >= H) break;
+      float x[kNormV], g[kNormV], ss = 0.f, dot = 0.f;
+      px[u].get(x);
+      pg[u].get(g);
+      if (a.R) turn.template turn<true>(g);
+#pragma unroll
+      for (int i = 0; i < kNormV; ++i) {
+        ss = __fmaf_rn(x[i], x[i], ss);
+        dot = __fmaf_rn(__fmul_rn(g[i], w[i]), x[i], dot);
+      }
+      ss = row_sum<LR>(ss);
+      dot = row_sum<LR>(dot);
+      const float rs = rsqrtf(__fmaf_rn(ss, a.inv_K, a.eps));
+      const float m = __fmul_rn(__fmul_rn(rs, rs), __fmul_rn(dot, a.inv_K));
+#pragma unroll
+      for (int i = 0; i < kNormV; ++i) {
+        gw[i] = __fmaf_rn(g[i], __fmul_rn(x[i], rs), gw[i]);  // x = 0 where there is no head
+        g[i] = __fmul_rn(rs, __fmaf_rn(-x[i], m, __fmul_rn(g[i], w[i])));
+      }
+      if (on && h0 + u * a.gpt < H) {
+        pg[u].set(g);
+        pg[u].store(gin + base + (int64_t)(h0 + u * a.gpt) * a.K);
+      }
     }
   }
 }
 
 // part: [2][gridDim.x][K] partial weight gradients (q, k).
 template <class E, int LR, bool IL>
-__global__ void __launch_bounds__(kNormThreads) norm_rotate_bwd_kernel(NormRows a, const E* __restrict__ q,
+__global__ void __launch_bounds__(kNormThreads, 2) norm_rotate_bwd_kernel(NormRows a, const E* __restrict__ q,
                                                                        const E* __restrict__ k, const E* gqo,
                                                                        const E* gko, const float* __restrict__ wq,
                                                                        const float* __restrict__ wk, E* gq, E* gk,
                                                                        float* __restrict__ part) {
-  extern __shared__ float tab[];
+  extern __shared__ float4 tab4[];
   __shared__ float sums[kNormThreads * kNormV];
-  float* cs = tab;
-  float* sn = tab + a.tok_cta * (a.R / 2);
-  const int l = threadIdx.x % LR, row_lane0 = (threadIdx.x % 32) / LR * LR;
+  constexpr int RP = kNormThreads / LR;
+  const int ntok = RP / a.gpt, row = norm_row(a.R);
+  float* cs = reinterpret_cast<float*>(tab4);
+  float* sn = cs + ntok * row;
+  const int l = threadIdx.x % LR, grp = threadIdx.x / LR, t = grp / a.gpt, hsub = grp % a.gpt;
   const bool on = l * kNormV < a.K;
   float w[2][kNormV], gw[2][kNormV];
   ld_param<kNormV>(wq && on ? wq + l * kNormV : nullptr, w[0], 1.f);
   ld_param<kNormV>(wk && on ? wk + l * kNormV : nullptr, w[1], 1.f);
 #pragma unroll
   for (int i = 0; i < kNormV; ++i) gw[0][i] = gw[1][i] = 0.f;
-  const int H = a.Hq + a.Hk;
-  constexpr int RP = kNormThreads / LR;
-  for (int64_t t0 = (int64_t)blockIdx.x * a.tok_cta; t0 < a.tokens; t0 += (int64_t)gridDim.x * a.tok_cta) {
-    const int nt = (int)min((int64_t)a.tok_cta, a.tokens - t0);
-    __syncthreads();  // the tables of the step before are done with
-    norm_angles(a, t0, nt, cs, sn);
-    __syncthreads();
-    const int rows = nt * H;
-    for (int r0 = 0; r0 < rows; r0 += RP) {
-      const int r = r0 + threadIdx.x / LR;
-      const bool have = r < rows && on;
-      const int t = r / H, h = r - t * H;
-      const bool key = h >= a.Hq;
-      const int64_t off = key ? ((t0 + t) * a.Hk + (h - a.Hq)) * (int64_t)a.K : ((t0 + t) * a.Hq + h) * (int64_t)a.K;
-      Pack<E, kNormV> px, pg;
-      px.zero();
-      pg.zero();
-      if (have) {
-        px.load((key ? k : q) + off + l * kNormV);
-        pg.load((key ? gko : gqo) + off + l * kNormV);
-      }
-      float x[kNormV], g[kNormV];
-      px.get(x);
-      pg.get(g);
-      if (a.R) {
-        const int tt = min(t, nt - 1) * (a.R / 2);
-        norm_turn<IL, true>(g, l, row_lane0, a.R, cs + tt, sn + tt);
-      }
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < kNormV; ++i) {
-        ss = __fmaf_rn(x[i], x[i], ss);
-        dot = __fmaf_rn(__fmul_rn(g[i], key ? w[1][i] : w[0][i]), x[i], dot);
-      }
-      ss = row_sum<LR>(ss);
-      dot = row_sum<LR>(dot);
-      const float rs = rsqrtf(__fmaf_rn(ss, a.inv_K, a.eps));
-      const float m = __fmul_rn(__fmul_rn(rs, rs), __fmul_rn(dot, a.inv_K));
-      float o[kNormV];
-#pragma unroll
-      for (int i = 0; i < kNormV; ++i) {
-        const float gx = __fmul_rn(g[i], __fmul_rn(x[i], rs));
-        if (have) {
-          if (key)
-            gw[1][i] = __fadd_rn(gw[1][i], gx);
-          else
-            gw[0][i] = __fadd_rn(gw[0][i], gx);
-        }
-        o[i] = __fmul_rn(rs, __fmaf_rn(-x[i], m, __fmul_rn(g[i], key ? w[1][i] : w[0][i])));
-      }
-      if (have) {
-        pg.set(o);
-        pg.store((key ? gk : gq) + off + l * kNormV);
-      }
+  for (int64_t t0 = (int64_t)blockIdx.x * ntok; t0 < a.tokens; t0 += (int64_t)gridDim.x * ntok) {
+    const int64_t left = a.tokens - t0;
+    NormTurn<IL> turn;
+    if (a.R) {
+      __syncthreads();  // the tables of the step before are done with
+      norm_angles(a, t0, (int)min((int64_t)ntok, left), cs, sn);
+      __syncthreads();
+      turn.load(cs + t * row, sn + t * row, l, (threadIdx.x % 32) / LR * LR, a.R);
     }
+    norm_heads_bwd<E, LR, IL>(a, q, gqo, gq, a.Hq, t0 + t, t < left, hsub, l, w[0], turn, gw[0]);
+    norm_heads_bwd<E, LR, IL>(a, k, gko, gk, a.Hk, t0 + t, t < left, hsub, l, w[1], turn, gw[1]);
   }
-  // the CTA's sums: thread i < LR * 8 adds element i of its RP rows in order
+  // the CTA's sums: thread i < K adds element i of its RP groups in order
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     __syncthreads();
@@ -226,12 +267,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotate_bwd_kernel(NormRows 
 
 int norm_lanes(int64_t K) { return K <= 8 ? 1 : K <= 16 ? 2 : K <= 32 ? 4 : K <= 64 ? 8 : K <= 128 ? 16 : 32; }
 
-// Tokens per CTA: rows for four passes of its threads.
-int norm_tokens(int64_t tokens, int64_t H, int64_t K) {
-  const int64_t rows = 4 * kNormThreads / norm_lanes(K);
-  const int64_t want = std::min<int64_t>(kNormMaxTokens, ceil_div(rows, std::max<int64_t>(1, H)));
-  // few tokens: spread them over the SMs instead
-  return (int)std::max<int64_t>(1, std::min(want, tokens / 148));
+// Groups of lanes per token: one for every 16 heads, whose work pays for the
+// group's share of the angles (one for every 8: 107 against 103 us at 32 + 32
+// heads of 64, 32,768 tokens), more where there are few tokens, so that they
+// spread over the SMs.
+int norm_gpt(int64_t tokens, int64_t H, int64_t K) {
+  const int64_t groups = kNormThreads / norm_lanes(K);
+  int gpt = 1;
+  while (gpt < groups && (gpt * 16 < H || (gpt < H && tokens * gpt < 148 * 2 * groups))) gpt *= 2;
+  return gpt;
 }
 
 NormRows norm_rows(const NormArgs& a) {
@@ -242,7 +286,7 @@ NormRows norm_rows(const NormArgs& a) {
   r.Hk = a.Hk;
   r.K = a.K;
   r.R = a.R;
-  r.tok_cta = norm_tokens(a.tokens, a.Hq + a.Hk, a.K);
+  r.gpt = norm_gpt(a.tokens, a.Hq + a.Hk, a.K);
   r.eps = a.eps;
   r.inv_K = 1.f / (float)a.K;
   r.inv_freq = a.inv_freq;
@@ -254,9 +298,10 @@ NormRows norm_rows(const NormArgs& a) {
 template <class E, int LR, bool IL>
 wkv_status run_norm(const NormArgs& a, bool bwd, cudaStream_t st, const char** why) {
   const NormRows r = norm_rows(a);
-  const size_t smem = (size_t)r.tok_cta * r.R * sizeof(float);
+  const int64_t ntok = kNormThreads / LR / r.gpt;
+  const size_t smem = r.R ? 2 * (size_t)ntok * norm_row(r.R) * sizeof(float) : 0;
   if (!bwd) {
-    norm_rotate_kernel<E, LR, IL><<<(unsigned)ceil_div(r.tokens, r.tok_cta), kNormThreads, smem, st>>>(
+    norm_rotate_kernel<E, LR, IL><<<(unsigned)ceil_div(r.tokens, ntok), kNormThreads, smem, st>>>(
         r, static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.wq, a.wk, static_cast<E*>(a.q_out),
         static_cast<E*>(a.k_out));
   } else {
@@ -294,7 +339,8 @@ wkv_status norm_dispatch(const NormArgs& a, bool bwd, cudaStream_t st, const cha
 }  // namespace
 
 int64_t norm_bwd_blocks(int64_t tokens, int64_t Hq, int64_t Hk, int64_t K) {
-  return std::min<int64_t>(ceil_div(tokens, norm_tokens(tokens, Hq + Hk, K)), 148 * 4);
+  const int64_t ntok = kNormThreads / norm_lanes(K) / norm_gpt(tokens, Hq + Hk, K);
+  return std::min<int64_t>(ceil_div(tokens, ntok), 148 * 2);
 }
 
 wkv_status launch_norm_rotate(const NormArgs& a, cudaStream_t stream, const char** why) {
@@ -303,10 +349,8 @@ wkv_status launch_norm_rotate(const NormArgs& a, cudaStream_t stream, const char
 
 wkv_status launch_norm_rotate_backward(const NormArgs& a, cudaStream_t stream, const char** why) {
   if (wkv_status s = norm_dispatch(a, true, stream, why)) return s;
-  const int64_t rows = norm_bwd_blocks(a.tokens, a.Hq, a.Hk, a.K);
-  if (a.gwq)
-    if (wkv_status s = launch_sum_rows(a.part, 1, rows, a.K, a.gwq, stream, why)) return s;
-  return a.gwk ? launch_sum_rows(a.part + rows * a.K, 1, rows, a.K, a.gwk, stream, why) : WKV_OK;
+  return launch_sum_rows(a.part, 2, norm_bwd_blocks(a.tokens, a.Hq, a.Hk, a.K), a.K, SumOutputs{{a.gwq, a.gwk}}, stream,
+                         why);
 }
 
 }  // namespace wkv

@@ -76,20 +76,6 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanParams& p) {
   return w;
 }
 
-// One copy of 8 or 16 bytes to shared memory that the thread does not wait
-// for; zeros where there is nothing to copy (src is then not read).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
-  static_assert(BYTES == 8 || BYTES == 16, "copy sizes");
-  const int n = there ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
 // A tile of tokens as stored: NT activations, B and C, with zeros past the
 // sequence, the group's channels and the N states.
 template <class E, class Geo, int NT>

@@ -492,10 +492,8 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
                                                                             static_cast<E*>(b.gC));
   if (wkv_status s = launched("scan gB, gC sum kernel launch failed", why)) return s;
   const int64_t rows = a.B * cut.nseg;
-  if (wkv_status s = launch_sum_rows(b.part_a, 1, rows, a.C * a.N, b.gA, st, why)) return s;
-  if (b.gD)
-    if (wkv_status s = launch_sum_rows(b.part_d, 1, rows, a.C, b.gD, st, why)) return s;
-  return b.gdt_bias ? launch_sum_rows(b.part_d + rows * a.C, 1, rows, a.C, b.gdt_bias, st, why) : WKV_OK;
+  if (wkv_status s = launch_sum_rows(b.part_a, 1, rows, a.C * a.N, SumOutputs{{b.gA}}, st, why)) return s;
+  return launch_sum_rows(b.part_d, 2, rows, a.C, SumOutputs{{b.gD, b.gdt_bias}}, st, why);
 }
 
 }  // namespace

@@ -289,12 +289,14 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
 #endif
 
 // Pieces along T: none where the channels alone give two CTAs per SM, since
-// the carry pass costs most of a second walk; else about four CTAs per SM,
-// pieces of at least 4 tiles.
+// the carry pass costs most of a second walk (B=2 C=4096, 256 CTAs, cut and
+// uncut: 217 and 209 us forward, 502 and 522 backward; B=4: 387 and 303, 921
+// and 852); else about eight CTAs per SM, which is what an SM holds (four: 205
+// against 176 us at B=1 T=8191 C=1536), in pieces of at least 4 tiles.
 ScanCut cut_for(int64_t ctas, int64_t T) {
   const int64_t tiles = std::max<int64_t>(1, ceil_div(T, kScanTile));
   int64_t nseg = 1;
-  if (ctas < 148 * 2) nseg = std::min(ceil_div(148 * 4, std::max<int64_t>(1, ctas)), std::max<int64_t>(1, tiles / 4));
+  if (ctas < 148 * 2) nseg = std::min(ceil_div(148 * 8, std::max<int64_t>(1, ctas)), std::max<int64_t>(1, tiles / 4));
   const int64_t per = ceil_div(tiles, nseg);
   return ScanCut{(int)ceil_div(tiles, per), (int)per};
 }
