@@ -47,14 +47,22 @@ for _name, (_res, _args) in SIGNATURES.items():
     getattr(_lib, _name).argtypes = _args
 
 
+# The current stream's handle without the torch.cuda.Stream object around it
+# (3 of the 15 microseconds a small call takes on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_fn = {name: getattr(_lib, name) for name in SIGNATURES}
+
+
 def _call(name: str, dev: torch.device, *args):
-    """Calls the C entry point with the stream appended, with `dev` current."""
-    fn = getattr(_lib, name)
+    """Calls the C entry point on the device's current stream, with `dev` current."""
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+        status = _fn[name](*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream), name)
+            status = _fn[name](*args, _raw_stream(dev.index))
+    if status:
+        _check(status, name)
 
 
 def _has(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
@@ -83,8 +91,8 @@ def _space(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
         if nbytes == 0:
             return None, 0, None
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    else:
-        _want(workspace, "workspace", device=dev)
+        return workspace.data_ptr(), nbytes, workspace
+    _want(workspace, "workspace", device=dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -124,9 +132,9 @@ def wkv_conv_backward(x, weight, gy, bias=None, x_prev=None, *, silu: bool = Tru
     B, T, C = x.shape
     W, f32 = _taps(weight, C), torch.float32
     gx = torch.empty_like(x) if gx is None else gx
-    gweight = torch.empty((W, C), dtype=f32, device=dev) if gweight is None else gweight
+    gweight = torch.empty_like(weight) if gweight is None else gweight
     if gbias is None and bias is not None:
-        gbias = torch.empty(C, dtype=f32, device=dev)
+        gbias = torch.empty_like(bias)
     if gx_prev is None and want_gx_prev:
         gx_prev = torch.empty((B, W - 1, C), dtype=x.dtype, device=dev)
     code = _dtype_code(x)
@@ -235,7 +243,7 @@ def wkv_norm_rotate_backward(q, k, gq_out, gk_out, q_weight=None, k_weight=None,
             _has(go, f"g{name}_out", dtype, t.shape, dev)
             _has(g, f"g{name}", dtype, t.shape, dev)
         grads.append(g if t is not None else None)
-        weights.append(None if w is None else torch.empty(K, dtype=torch.float32, device=dev))
+        weights.append(None if w is None else torch.empty_like(w))
     p = [None if t is None else t.data_ptr() for t in
          (q, k, gq_out if q is not None else None, gk_out if k is not None else None, *grads, *weights)]
     ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, K)), dev)
