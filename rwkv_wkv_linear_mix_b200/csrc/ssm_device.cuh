@@ -130,15 +130,16 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
 }
 
 // One copy of 8 or 16 bytes to shared memory that the thread does not wait
-// for; zeros where there is nothing to copy (src is then not read).
+// for; zeros where there is nothing to copy (src is then not read). dst: a
+// shared-memory address.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
   static_assert(BYTES == 8 || BYTES == 16, "copy sizes");
   const int n = there ? BYTES : 0;
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most LEFT of the thread's groups of copies are in flight.

@@ -83,28 +83,6 @@ struct ScanRaw {
   E act[NT][kScanTile][Geo::CB];
   E bc[2][kScanTile][Geo::NP];
 
-  // at: token t0 of the sequence times C, plus c0; left: tokens from t0 to the end
-  __device__ __forceinline__ void load_act(int which, const E* base, int64_t at, int64_t C, int left, int channels) {
-#pragma unroll
-    for (int i = 0; i < (kScanTile * Geo::VPR + Geo::THREADS - 1) / Geo::THREADS; ++i) {
-      const int k = (int)threadIdx.x + i * Geo::THREADS, t = k / Geo::VPR, col = k % Geo::VPR * Geo::VN;
-      if (t < kScanTile) {
-        const bool there = t < left && col < channels;
-        copy_async<16>(&act[which][t][col], there ? base + at + t * C + col : base, there);
-      }
-    }
-  }
-  // at: token t0 times G N, plus the group's first state
-  __device__ __forceinline__ void load_bc(int which, const E* base, int64_t at, int64_t GN, int left, int N) {
-#pragma unroll
-    for (int i = 0; i < (kScanTile * Geo::BPR + Geo::THREADS - 1) / Geo::THREADS; ++i) {
-      const int k = (int)threadIdx.x + i * Geo::THREADS, t = k / Geo::BPR, n = k % Geo::BPR * 4;
-      if (t < kScanTile) {
-        const bool there = t < left && n < N;
-        copy_async<4 * (int)sizeof(E)>(&bc[which][t][n], there ? base + at + t * GN + n : base, there);
-      }
-    }
-  }
   // B or C into float32 rows [16][V][NP], row m of a token with state n at n ^ m
   template <int V>
   __device__ __forceinline__ void put_bc(int which, float* table) const {
@@ -122,6 +100,62 @@ struct ScanRaw {
               make_float4(f[m], f[1 ^ m], f[2 ^ m], f[3 ^ m]);
       }
     }
+  }
+};
+
+// The copies of a tile that a thread issues: what to read, where to and which
+// token, worked out once and moved on tile by tile (worked out anew for each
+// tile they were 8 % of the forward's instructions).
+template <class E, class Geo, int NT>
+struct ScanCopies {
+  static constexpr int ACTS = kScanTile * Geo::VPR, PA = (NT * ACTS + Geo::THREADS - 1) / Geo::THREADS;
+  static constexpr int BCS = kScanTile * Geo::BPR, PB = (2 * BCS + Geo::THREADS - 1) / Geo::THREADS;
+  static constexpr int kNone = 1 << 20;  // no token: zeros
+  const E *a[PA], *b[PB];
+  uint32_t a_to[PA], b_to[PB];
+  int a_t[PA], b_t[PB];
+
+  // From the tile whose first token is row `row` of the tensors; a tensor may be null.
+  __device__ __forceinline__ void init(ScanRaw<E, Geo, NT>& raw, const void* const (&act)[NT], const void* const (&bc)[2],
+                                       int64_t row, int64_t C, int64_t c0, int channels, int64_t GN, int64_t gN, int N) {
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int k = (int)threadIdx.x + i * Geo::THREADS, w = k / ACTS % NT, t = k % ACTS / Geo::VPR,
+                col = k % Geo::VPR * Geo::VN;
+      const void* from = act[0];
+#pragma unroll
+      for (int j = 1; j < NT; ++j) from = w == j ? act[j] : from;
+      a_t[i] = from && col < channels ? t : kNone;
+      a[i] = static_cast<const E*>(from) + (row + t) * C + c0 + col;
+      a_to[i] = smem_u32(&raw.act[w][t][col]);
+    }
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const int k = (int)threadIdx.x + i * Geo::THREADS, w = k / BCS % 2, t = k % BCS / Geo::BPR, n = k % Geo::BPR * 4;
+      const void* from = w ? bc[1] : bc[0];
+      b_t[i] = from && n < N ? t : kNone;
+      b[i] = static_cast<const E*>(from) + (row + t) * GN + gN + n;
+      b_to[i] = smem_u32(&raw.bc[w][t][n]);
+    }
+  }
+  // The tile with `left` tokens, into the raw tile `offset` bytes after the first.
+  __device__ __forceinline__ void issue(uint32_t offset, int left) const {
+#pragma unroll
+    for (int i = 0; i < PA; ++i)
+      if ((NT * ACTS) % Geo::THREADS == 0 || (int)threadIdx.x + i * Geo::THREADS < NT * ACTS)
+        copy_async<16>(a_to[i] + offset, a[i], a_t[i] < left);
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+      if ((2 * BCS) % Geo::THREADS == 0 || (int)threadIdx.x + i * Geo::THREADS < 2 * BCS)
+        copy_async<4 * (int)sizeof(E)>(b_to[i] + offset, b[i], b_t[i] < left);
+    copy_async_commit();
+  }
+  // On by so many rows of the activations and of B and C, in elements.
+  __device__ __forceinline__ void step(int64_t by_a, int64_t by_b) {
+#pragma unroll
+    for (int i = 0; i < PA; ++i) a[i] += by_a;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) b[i] += by_b;
   }
 };
 
@@ -263,11 +297,10 @@ template <int LPC>
 __device__ __forceinline__ int pair_sum_first(int g) {
   return reduce_scatter_first<4, LPC / 2>(g / 2);
 }
+// The first step, for one token; then the rest, for four.
+__device__ __forceinline__ float pair_give(float2 s) { return __fadd_rn(s.x, __shfl_xor_sync(0xffffffffu, s.y, 1)); }
 template <int LPC>
-__device__ __forceinline__ void pair_sums(const float2 (&s)[4], float (&out)[kPairSums<LPC>], int lane) {
-  float v[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) v[t] = __fadd_rn(s[t].x, __shfl_xor_sync(0xffffffffu, s[t].y, 1));
+__device__ __forceinline__ void pair_sums(float (&v)[4], float (&out)[kPairSums<LPC>], int lane) {
   reduce_scatter<4, LPC / 2, 2>(v, lane);
 #pragma unroll
   for (int t = 0; t < kPairSums<LPC>; ++t) out[t] = v[t];

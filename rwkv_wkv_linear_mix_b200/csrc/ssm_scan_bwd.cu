@@ -35,15 +35,16 @@ template <class E, class Geo>
 struct ScanBwdShared {
   static constexpr int WARPS = Geo::THREADS / 32;
   ScanRaw<E, Geo, kActs> raw;                    // the tile that is next
-  // rows padded by a pair (32 bytes), since lanes that finish outputs read 4 tokens at once
-  float4 dd[kScanTile][Geo::HB + 1][2];          // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
-  float4 gx[kScanTile][Geo::HB + 1][2];          // gs0, gs1, x0, x1; and swapped
-  float2 sz[kScanTile][Geo::HB + 2][2];          // per channel: softplus'(raw), gy silu'(z)
+  float4 dd[kScanTile][Geo::HB][2];              // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
+  float2 gs[kScanTile][Geo::HB][2];              // gs0, gs1; and swapped
+  // per channel, to finish with: d, x, softplus'(raw), gy silu'(z) (rows a
+  // pair apart, since the lanes read 4 tokens at once)
+  float4 fin[kScanTile][Geo::HB + 1][2];
   float B[kScanTile][Geo::S][Geo::NP];           // in each order of a lane's states
   float C[kScanTile][Geo::S][Geo::NP];
   float sum[2][WARPS][kScanTile][Geo::NP];       // gB, gC of each warp's channels
-  // the states before token 0, SUB, 2 SUB, ... of the tile, per thread and channel
-  float h[kScanTile / kBwdSub][2][Geo::THREADS][Geo::S];
+  // the states before token 0, SUB, 2 SUB, ... of the tile but the last, per thread and channel
+  float h[kScanTile / kBwdSub - 1][2][Geo::THREADS][Geo::S];
 };
 
 // Sums over the lanes that hold the same states of other channel pairs (lane
@@ -112,17 +113,15 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
   auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
   auto tokens = [&](int i) { return (int)min(tend - start(i), (int64_t)kScanTile); };
 
-  auto load = [&](int i) {
-    ScanRaw<E, Geo, kActs>& r = sm.raw;
-    const int left = tokens(i);
-    const int64_t at = (first + start(i)) * p.C + w.c0, bc = (first + start(i)) * GN + gN;
-    r.load_act(kActX, static_cast<const E*>(p.x), at, p.C, left, channels);
-    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
-    r.load_act(kActGy, static_cast<const E*>(p.gy), at, p.C, left, channels);
-    if constexpr (Z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
-    r.load_bc(0, static_cast<const E*>(p.Bm), bc, GN, left, (int)p.N);
-    r.load_bc(1, static_cast<const E*>(p.Cm), bc, GN, left, (int)p.N);
-    copy_async_commit();
+  ScanCopies<E, Geo, kActs> copies;
+  {
+    const void* const act[kActs] = {p.x, p.dt, p.gy, Z ? p.z : nullptr};
+    const void* const bc[2] = {p.Bm, p.Cm};
+    copies.init(sm.raw, act, bc, first + start(nt - 1), p.C, w.c0, channels, GN, gN, (int)p.N);
+  }
+  auto load = [&](int i) {  // from the last tile down
+    copies.issue(0, tokens(i));
+    copies.step(-kScanTile * p.C, -kScanTile * GN);
   };
   const int lp = tid % Geo::HB;
   const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);
@@ -150,9 +149,9 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
       const float2 dx = mul2(d, x);
       sm.dd[t][lp][0] = make_float4(d.x, d.y, dx.x, dx.y);
       sm.dd[t][lp][1] = make_float4(d.y, d.x, dx.y, dx.x);
-      sm.gx[t][lp][0] = make_float4(gs.x, gs.y, x.x, x.y);
-      sm.gx[t][lp][1] = make_float4(gs.y, gs.x, x.y, x.x);
-      *reinterpret_cast<float4*>(sm.sz[t][lp]) = make_float4(sp.x, gz.x, sp.y, gz.y);
+      *reinterpret_cast<float4*>(sm.gs[t][lp]) = make_float4(gs.x, gs.y, gs.y, gs.x);
+      sm.fin[t][lp][0] = make_float4(d.x, x.x, sp.x, gz.x);
+      sm.fin[t][lp][1] = make_float4(d.y, x.y, sp.y, gz.y);
     }
   };
 
@@ -224,78 +223,75 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
     convert(i);
     __syncthreads();
     if (i > 0) load(i - 1);
+    const int64_t at = (first + t0) * p.C + c + order.swap;
     st_h(0, h);
     // up to the last SUB tokens, leaving the states on the way
 #pragma unroll
     for (int t = 0; t < kScanTile - SUB; ++t) {
       const float4 dd = sm.dd[t][pair][order.swap];
       scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[t][order.perm][S * g]));
-      if ((t + 1) % SUB == 0) st_h((t + 1) / SUB, h);
+      if ((t + 1) % SUB == 0 && t + 1 < kScanTile - SUB) st_h((t + 1) / SUB, h);
     }
 #pragma unroll 1
     for (int sub = kScanTile / SUB - 1; sub >= 0; --sub) {
       const int tb = sub * SUB;
-      {
+      if (sub < kScanTile / SUB - 1) {
         const Row<S> a = ld_row<S>(sm.h[sub][0][tid]), b = ld_row<S>(sm.h[sub][1][tid]);
 #pragma unroll
         for (int j = 0; j < S; ++j) h.n[j] = make_float2(a.n[j], b.n[j]);
       }
-      // up: the decays and decayed states, gC and s. Nothing is stored before
-      // the end of the sub-block: a store would hold back the shared-memory
-      // loads behind it.
+      // up: the decays and decayed states
       States<S> a[SUB], ah[SUB];
-      float gc[SUB / 2][Sums::GV], gb[SUB / 2][Sums::GV], sv[kPairSums<LPC>];
-      float2 s4[SUB];
 #pragma unroll
-      for (int t = 0; t < SUB; t += 2) {
-        float r[2][S];
+      for (int t = 0; t < SUB; ++t) {
+        const float4 dd = sm.dd[tb + t][pair][order.swap];
+        const Row<S> Bv = ld_row<S>(&sm.B[tb + t][order.perm][S * g]);
+        a[t] = scan_decay(make_float2(dd.x, dd.y), A2);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float4 dd = sm.dd[tb + t + u][pair][order.swap];
-          const float2 gs = *reinterpret_cast<const float2*>(&sm.gx[tb + t + u][pair][order.swap]);
-          const Row<S> Bv = ld_row<S>(&sm.B[tb + t + u][order.perm][S * g]);
-          a[t + u] = scan_decay(make_float2(dd.x, dd.y), A2);
-#pragma unroll
-          for (int j = 0; j < S; ++j) {
-            ah[t + u].n[j] = mul2(a[t + u].n[j], h.n[j]);
-            h.n[j] = fma2(make_float2(dd.z, dd.w), splat2(Bv.n[j]), ah[t + u].n[j]);
-            const float2 s = mul2(gs, h.n[j]);
-            r[u][j] = __fadd_rn(s.x, s.y);
-          }
-          if constexpr (Z) s4[t + u] = scan_dot<S>(h, ld_row<S>(&sm.C[tb + t + u][order.perm][S * g]));
+        for (int j = 0; j < S; ++j) {
+          ah[t].n[j] = mul2(a[t].n[j], h.n[j]);
+          h.n[j] = fma2(make_float2(dd.z, dd.w), splat2(Bv.n[j]), ah[t].n[j]);
         }
-        Sums::sum(r, gc[t / 2], lane);
       }
-      if constexpr (Z) pair_sums<LPC>(s4, sv, lane);
-      // down again
-      float2 qb[SUB], wa[SUB];  // sum Q B, sum A2 Q a h
+      // down again, the states formed anew from the decayed ones (which is
+      // cheaper than to read gs and C on the way up too: the kernel is bound
+      // by what it reads of shared memory). Nothing is stored before the end
+      // of the sub-block: a store would hold back the loads behind it.
+      float gc[SUB / 2][Sums::GV], gb[SUB / 2][Sums::GV];
+      float qb[SUB], wa[SUB], s4[SUB];  // sum Q B, sum A2 Q a h, sum C h
 #pragma unroll
       for (int t = SUB - 2; t >= 0; t -= 2) {
-        float r[2][S];
+        float rb[2][S], rc[2][S];
 #pragma unroll
         for (int u = 1; u >= 0; --u) {
           const int tt = tb + t + u;
           const float4 dd = sm.dd[tt][pair][order.swap];
-          const float2 gs = *reinterpret_cast<const float2*>(&sm.gx[tt][pair][order.swap]);
-          const Row<S> Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
-          States<S> Q, W;
+          const float2 gs = sm.gs[tt][pair][order.swap];
+          const Row<S> Bv = ld_row<S>(&sm.B[tt][order.perm][S * g]), Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
+          const float2 d = make_float2(dd.x, dd.y), dx = make_float2(dd.z, dd.w);
+          States<S> Q, W, ht;
 #pragma unroll
           for (int j = 0; j < S; ++j) {
+            ht.n[j] = fma2(dx, splat2(Bv.n[j]), ah[t + u].n[j]);
             Q.n[j] = fma2(gs, splat2(Cv.n[j]), q.n[j]);
             q.n[j] = mul2(a[t + u].n[j], Q.n[j]);
             W.n[j] = mul2(Q.n[j], ah[t + u].n[j]);
-            gA.n[j] = fma2(make_float2(dd.x, dd.y), W.n[j], gA.n[j]);
-            const float2 s = mul2(make_float2(dd.z, dd.w), Q.n[j]);
-            r[u][j] = __fadd_rn(s.x, s.y);
+            gA.n[j] = fma2(d, W.n[j], gA.n[j]);
+            const float2 sb = mul2(dx, Q.n[j]), sc = mul2(gs, ht.n[j]);
+            rb[u][j] = __fadd_rn(sb.x, sb.y);
+            rc[u][j] = __fadd_rn(sc.x, sc.y);
           }
-          qb[t + u] = scan_dot<S>(Q, ld_row<S>(&sm.B[tt][order.perm][S * g]));
-          wa[t + u] = scan_dot<S>(W, A2);
+          qb[t + u] = pair_give(scan_dot<S>(Q, Bv));
+          wa[t + u] = pair_give(scan_dot<S>(W, A2));
+          if constexpr (Z) s4[t + u] = pair_give(scan_dot<S>(ht, Cv));
         }
-        Sums::sum(r, gb[t / 2], lane);
+        Sums::sum(rb, gb[t / 2], lane);
+        Sums::sum(rc, gc[t / 2], lane);
       }
-      float out[kPairSums<LPC>], out2[kPairSums<LPC>];
+      float out[kPairSums<LPC>], out2[kPairSums<LPC>], sv[kPairSums<LPC>];
       pair_sums<LPC>(qb, out, lane);
       pair_sums<LPC>(wa, out2, lane);
+      if constexpr (Z) pair_sums<LPC>(s4, sv, lane);
       // the sub-block's results
 #pragma unroll
       for (int t = 0; t < SUB; t += 2)
@@ -305,21 +301,20 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
           sm.sum[1][warp][tt][n] = gc[t / 2][v];
           sm.sum[0][warp][tt][n] = gb[t / 2][v];
         }
-      const int64_t at = (first + t0) * p.C + c + order.swap;
 #pragma unroll
       for (int v = 0; v < kPairSums<LPC>; ++v) {
         const int tt = tb + pair_sum_first<LPC>(g) + v;
-        const float d = sm.dd[tt][pair][order.swap].x;
-        const float4 gx = sm.gx[tt][pair][order.swap];
-        const float2 sz = sm.sz[tt][pair][order.swap];
-        const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gx.x, D));
-        const float graw = __fmul_rn(__fmaf_rn(out[v], gx.z, __fmul_rn(out2[v], 1.f / kLog2e)), sz.x);
+        const float4 fin = sm.fin[tt][pair][order.swap];
+        const float d = fin.x, x = fin.y, gs = sm.gs[tt][pair][order.swap].x;
+        const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gs, D));
+        const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
         if (tt < left && ch_on && g < 8) {
-          static_cast<E*>(p.gx)[at + tt * p.C] = Elem<E>::from_f32(rgx);
-          static_cast<E*>(p.gdt)[at + tt * p.C] = Elem<E>::from_f32(graw);
+          const int64_t to = at + tt * (int)p.C;
+          static_cast<E*>(p.gx)[to] = Elem<E>::from_f32(rgx);
+          static_cast<E*>(p.gdt)[to] = Elem<E>::from_f32(graw);
           if constexpr (Z)
-            static_cast<E*>(p.gz)[at + tt * p.C] = Elem<E>::from_f32(__fmul_rn(sz.y, __fmaf_rn(D, gx.z, sv[v])));
-          gD = __fmaf_rn(gx.x, gx.z, gD);
+            static_cast<E*>(p.gz)[to] = Elem<E>::from_f32(__fmul_rn(fin.w, __fmaf_rn(D, x, sv[v])));
+          gD = __fmaf_rn(gs, x, gD);
           gdb = __fadd_rn(gdb, graw);
         }
       }
@@ -368,15 +363,15 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_bwd_carry_k
   const int channels = (int)(w.cend - w.c0);
   auto start = [&](int i) { return tbeg + (int64_t)i * kScanTile; };
   auto tokens = [&](int i) { return (int)min(tend - start(i), (int64_t)kScanTile); };
-  auto load = [&](int i) {
-    ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
-    const int left = tokens(i);
-    const int64_t at = (first + start(i)) * p.C + w.c0;
-    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
-    r.load_act(kActGy, static_cast<const E*>(p.gy), at, p.C, left, channels);
-    if (p.z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
-    r.load_bc(1, static_cast<const E*>(p.Cm), (first + start(i)) * GN + w.g * p.N, GN, left, (int)p.N);
-    copy_async_commit();
+  ScanCopies<E, Geo, kActs> copies;
+  {
+    const void* const act[kActs] = {nullptr, p.dt, p.gy, p.z};
+    const void* const bc[2] = {nullptr, p.Cm};
+    copies.init(sm.raw[0], act, bc, first + start(nt - 1), p.C, w.c0, channels, GN, w.g * p.N, (int)p.N);
+  }
+  auto load = [&](int i) {  // from the last tile down
+    copies.issue((i & 1) * (uint32_t)sizeof(sm.raw[0]), tokens(i));
+    copies.step(-kScanTile * p.C, -kScanTile * GN);
   };
   const int lp = tid % Geo::HB;
   const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);

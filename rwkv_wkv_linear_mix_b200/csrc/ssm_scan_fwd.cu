@@ -37,8 +37,11 @@ struct ScanFwdShared {
   float C[kScanTile][Geo::NP];
 };
 
+// Seven CTAs of 4 warps per SM with two states per lane (72 registers): left
+// alone the compiler takes up to 168 (prompt, B=8 C=4096: 536 us against 452;
+// 9 CTAs, 56 registers: 463).
 template <class E, int LPC, int S, int MODE>
-__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_fwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) scan_fwd_kernel(const ScanParams p) {
   using Geo = ScanGeom<E, LPC, S>;
   extern __shared__ float4 smem4[];
   auto& sm = *reinterpret_cast<ScanFwdShared<E, Geo>*>(smem4);
@@ -62,19 +65,15 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_fwd_kernel(
   const int64_t GN = p.G * p.N;
   const int channels = (int)(w.cend - w.c0);
 
+  ScanCopies<E, Geo, kActs> copies;
+  {
+    const void* const act[kActs] = {p.x, p.dt, MODE != kScanCarry ? p.z : nullptr};
+    const void* const bc[2] = {p.Bm, MODE != kScanCarry ? p.Cm : nullptr};
+    copies.init(sm.raw[0], act, bc, first + tbeg, p.C, w.c0, channels, GN, w.g * p.N, (int)p.N);
+  }
   auto load = [&](int i) {
-    ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
-    const int64_t t0 = tbeg + (int64_t)i * kScanTile;
-    const int left = (int)min(tend - t0, (int64_t)kScanTile);
-    const int64_t at = (first + t0) * p.C + w.c0, bc = (first + t0) * GN + w.g * p.N;
-    r.load_act(kActX, static_cast<const E*>(p.x), at, p.C, left, channels);
-    r.load_act(kActDt, static_cast<const E*>(p.dt), at, p.C, left, channels);
-    r.load_bc(0, static_cast<const E*>(p.Bm), bc, GN, left, (int)p.N);
-    if constexpr (MODE != kScanCarry) {
-      r.load_bc(1, static_cast<const E*>(p.Cm), bc, GN, left, (int)p.N);
-      if (p.z) r.load_act(kActZ, static_cast<const E*>(p.z), at, p.C, left, channels);
-    }
-    copy_async_commit();
+    copies.issue((i & 1) * (uint32_t)sizeof(sm.raw[0]), (int)min(tend - tbeg - (int64_t)i * kScanTile, (int64_t)kScanTile));
+    copies.step(kScanTile * p.C, kScanTile * GN);
   };
   // the thread's channel pair in the conversion
   const int lp = tid % Geo::HB;
@@ -133,18 +132,23 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_fwd_kernel(
     float done[kScanTile / 4][kPairSums<LPC>];  // stored after the walk: a store would hold back the loads behind it
 #pragma unroll
     for (int tg = 0; tg < kScanTile; tg += 4) {
-      float2 out[4];
+      float2 dots[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 dd = sm.dd[tg + j][pair][swap];
         const float2 d = make_float2(dd.x, dd.y);
         scan_absorb(h, scan_decay(d, A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[tg + j][S * g]));
         if constexpr (MODE != kScanCarry)
-          out[j] = scan_dot<S>(h, ld_row<S>(&sm.C[tg + j][S * g]));
+          dots[j] = scan_dot<S>(h, ld_row<S>(&sm.C[tg + j][S * g]));
         else
           tile_d = add2(tile_d, d);
       }
-      if constexpr (MODE != kScanCarry) pair_sums<LPC>(out, done[tg / 4], tid);
+      if constexpr (MODE != kScanCarry) {
+        float out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[j] = pair_give(dots[j]);
+        pair_sums<LPC>(out, done[tg / 4], tid);
+      }
     }
     if (MODE != kScanCarry && p.y) {
       // done[tg / 4][v]: channel `swap` of token tg + out0 + v
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_fwd_kernel(
             const float z = Elem<E>::to_f32(r.act[kActZ][t][2 * pair + swap]);
             o = __fmul_rn(o, __fmul_rn(z, sigmoid_f(z)));
           }
-          if (t < left) y[t * p.C] = Elem<E>::from_f32(o);
+          if (t < left) y[t * (int)p.C] = Elem<E>::from_f32(o);
         }
       }
     }
