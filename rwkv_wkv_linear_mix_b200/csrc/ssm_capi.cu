@@ -35,11 +35,12 @@ wkv_status check_act(int64_t B, int64_t T, int64_t C, int dtype) {
   if (dtype != WKV_F32 && dtype != WKV_BF16) return fail(WKV_ERR_INVALID_ARG, "unknown dtype");
   if ((dtype == WKV_F32 && C % 4) || (dtype == WKV_BF16 && C % 8))
     return fail(WKV_ERR_UNSUPPORTED, "C must be a multiple of 4 (f32) or 8 (bf16)");
-  if (T > INT32_MAX || C > INT32_MAX || B > INT32_MAX) return fail(WKV_ERR_UNSUPPORTED, "size above 2^31-1");
+  if (T > INT32_MAX || B > INT32_MAX) return fail(WKV_ERR_UNSUPPORTED, "size above 2^31-1");
+  if (C > (1 << 26)) return fail(WKV_ERR_UNSUPPORTED, "C above 2^26");
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (B > 0 && C > 0 && (B > kMost / C || (T > 0 && B * C > kMost / T)))
     return fail(WKV_ERR_UNSUPPORTED, "problem above 2^40 elements");
-  if (B * ceil_div(C, 32) > INT32_MAX / 4096) return fail(WKV_ERR_UNSUPPORTED, "B * C too large for one launch");
+  if (B * ceil_div(C, 32) > (1 << 26)) return fail(WKV_ERR_UNSUPPORTED, "B * C too large for one launch");
   return WKV_OK;
 }
 
@@ -282,6 +283,8 @@ static wkv_status check_scan(int64_t B, int64_t T, int64_t C, int64_t N, int64_t
   if ((C / G) % unit) return fail(WKV_ERR_UNSUPPORTED, "C / G must be a multiple of 4 (f32) or 8 (bf16)");
   if (B > 0 && C > 0 && ceil_div(std::max<int64_t>(T, 1), WKV_SCAN_CKPT_LEN) > ((int64_t)1 << 40) / N / (B * C))
     return fail(WKV_ERR_UNSUPPORTED, "state checkpoints above 2^40 elements");
+  if (B > 0 && T > 0 && B * T > ((int64_t)1 << 40) / (G * N))
+    return fail(WKV_ERR_UNSUPPORTED, "B and C above 2^40 elements");
   return WKV_OK;
 }
 

@@ -59,28 +59,24 @@ struct NormTurn {
   static constexpr int NF = IL ? kNormV / 2 : kNormV;
   float c[NF], s[NF];  // s: with the sign of the other half's term
   int src;             // lane of the other half of the pairs
-  bool in;             // whether the lane's entries turn (interleaved: see R)
-  // cs, sn: the token's rows
-  __device__ __forceinline__ void load(const float* cs, const float* sn, int l, int row_lane0, int R) {
+  int turned;          // how many of the NF factors apply (entries from R on are left as they are)
+  // cs, sn: the token's rows, read only if `there`
+  __device__ __forceinline__ void load(const float* cs, const float* sn, bool there, int l, int row_lane0, int R) {
     const int lanes = R / (2 * kNormV);  // lanes that hold the first half
-    const bool lo = l < lanes;
-    in = IL ? l * kNormV < R : l < 2 * lanes;
+    const bool lo = l < lanes, in = l < 2 * lanes;
+    turned = !there ? 0 : IL ? min(max(R / 2 - l * NF, 0), NF) : in ? NF : 0;
     src = row_lane0 + (lo ? l + lanes : in ? l - lanes : l);
     const int f0 = IL ? l * NF : (lo ? l : l - lanes) * kNormV;
 #pragma unroll
     for (int i = 0; i < NF; ++i) c[i] = 1.f, s[i] = 0.f;
-    if (in) {
+    if (turned) {
 #pragma unroll
       for (int i = 0; i < NF; i += 4) {
         const float4 a = *reinterpret_cast<const float4*>(cs + f0 + i), b = *reinterpret_cast<const float4*>(sn + f0 + i);
         c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
         s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
       }
-      if (IL) {
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-          if (l * kNormV + 2 * i >= R) c[i] = 1.f, s[i] = 0.f;
-      } else if (lo) {
+      if (!IL && lo) {
 #pragma unroll
         for (int i = 0; i < NF; ++i) s[i] = -s[i];
       }
@@ -92,15 +88,17 @@ struct NormTurn {
     if constexpr (IL) {
 #pragma unroll
       for (int m = 0; m < NF; ++m) {
-        const float ss = BACK ? -s[m] : s[m], x = v[2 * m], y = v[2 * m + 1];
-        v[2 * m] = __fmaf_rn(x, c[m], -__fmul_rn(y, ss));
-        v[2 * m + 1] = __fmaf_rn(x, ss, __fmul_rn(y, c[m]));
+        if (m < turned) {
+          const float ss = BACK ? -s[m] : s[m], x = v[2 * m], y = v[2 * m + 1];
+          v[2 * m] = __fmaf_rn(x, c[m], -__fmul_rn(y, ss));
+          v[2 * m + 1] = __fmaf_rn(x, ss, __fmul_rn(y, c[m]));
+        }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kNormV; ++i) {
         const float other = __shfl_sync(0xffffffffu, v[i], src);
-        v[i] = __fmaf_rn(v[i], c[i], __fmul_rn(other, BACK ? -s[i] : s[i]));
+        if (turned) v[i] = __fmaf_rn(v[i], c[i], __fmul_rn(other, BACK ? -s[i] : s[i]));
       }
     }
   }
@@ -165,7 +163,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotate_kernel(NormRows a, c
   if (a.R) {
     norm_angles(a, t0, (int)min((int64_t)ntok, left), cs, sn);
     __syncthreads();
-    turn.load(cs + t * row, sn + t * row, l, (threadIdx.x % 32) / LR * LR, a.R);
+    turn.load(cs + t * row, sn + t * row, t < left, l, (threadIdx.x % 32) / LR * LR, a.R);
   }
   norm_heads<E, LR, IL>(a, q, q_out, a.Hq, t0 + t, t < left, hsub, l, wq, turn);
   norm_heads<E, LR, IL>(a, k, k_out, a.Hk, t0 + t, t < left, hsub, l, wk, turn);
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rotate_bwd_kernel(NormRo
       __syncthreads();  // the tables of the step before are done with
       norm_angles(a, t0, (int)min((int64_t)ntok, left), cs, sn);
       __syncthreads();
-      turn.load(cs + t * row, sn + t * row, l, (threadIdx.x % 32) / LR * LR, a.R);
+      turn.load(cs + t * row, sn + t * row, t < left, l, (threadIdx.x % 32) / LR * LR, a.R);
     }
     norm_heads_bwd<E, LR, IL>(a, q, gqo, gq, a.Hq, t0 + t, t < left, hsub, l, w[0], turn, gw[0]);
     norm_heads_bwd<E, LR, IL>(a, k, gko, gk, a.Hk, t0 + t, t < left, hsub, l, w[1], turn, gw[1]);

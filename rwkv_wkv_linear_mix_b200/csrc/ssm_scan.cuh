@@ -46,6 +46,7 @@ struct ScanParams {
   const float *A, *D, *dt_bias, *init_state;
   void* y;
   float *final_state, *ckpt, *carry;
+  int64_t final_step;  // floats between the final states of two sequences
   const int32_t* cu;
   int64_t n_tokens;
   unsigned* err;
@@ -317,6 +318,7 @@ inline ScanParams scan_params(const ScanArgs& a, const ScanCut& cut) {
   p.x = a.x, p.dt = a.dt, p.Bm = a.Bm, p.Cm = a.Cm, p.z = a.z;
   p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.init_state = a.init_state;
   p.y = a.y, p.final_state = a.final_state, p.ckpt = a.ckpt, p.carry = a.carry;
+  p.final_step = a.C * a.N;
   p.cu = a.cu, p.n_tokens = a.n_tokens;
   return p;
 }

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
     if (on) st_states_wide<S>(p.carry + row * p.N + S * g, p.N, h, swap);
     if (on && g == 0) st_pair(p.carry + p.B * p.nseg * p.C * p.N + row, sum_d);
   } else if (p.final_state && on && (MODE == kScanSlots || w.seg == p.nseg - 1)) {
-    st_states_wide<S>(p.final_state + state_at, p.N, h, swap);
+    st_states_wide<S>(p.final_state + w.b * p.final_step + c * p.N + S * g, p.N, h, swap);
   }
 }
 
@@ -255,10 +255,23 @@ wkv_status run_walk(const ScanParams& p, cudaStream_t st, const char** why) {
 template <class E, int LPC, int S>
 wkv_status run_forward(const ScanArgs& a, cudaStream_t st, const char** why) {
   const ScanCut cut = scan_fwd_cut(a.B, a.T, a.C, a.N, a.G);
-  const ScanParams p = scan_params(a, cut);
-  if (cut.nseg > 1)
-    if (wkv_status s = run_walk<E, LPC, S, kScanCarry>(p, st, why)) return s;
-  return run_walk<E, LPC, S, kScanMain>(p, st, why);
+  ScanParams p = scan_params(a, cut);
+  if (cut.nseg == 1) return run_walk<E, LPC, S, kScanMain>(p, st, why);
+  if (wkv_status s = run_walk<E, LPC, S, kScanCarry>(p, st, why)) return s;
+  if (!a.final_state || a.final_state != a.init_state) return run_walk<E, LPC, S, kScanMain>(p, st, why);
+  // In place: every piece reads the initial state, so the last one leaves the
+  // final state in its own (otherwise unused) slot among the pieces, and it
+  // is copied out once all have run.
+  p.final_state = p.carry + (cut.nseg - 1) * a.C * a.N;
+  p.final_step = cut.nseg * a.C * a.N;
+  if (wkv_status s = run_walk<E, LPC, S, kScanMain>(p, st, why)) return s;
+  const size_t row = (size_t)a.C * a.N * sizeof(float);
+  if (cudaMemcpy2DAsync(a.final_state, row, p.final_state, cut.nseg * row, row, (size_t)a.B, cudaMemcpyDeviceToDevice, st) !=
+      cudaSuccess) {
+    *why = "copy of the final state failed";
+    return WKV_ERR_CUDA;
+  }
+  return WKV_OK;
 }
 template <class E, int LPC, int S>
 wkv_status run_slots(const ScanArgs& a, cudaStream_t st, unsigned* err, const char** why) {

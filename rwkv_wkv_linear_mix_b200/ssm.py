@@ -181,6 +181,8 @@ def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: boo
 
 def _heads(q, k, head_size):
     """(device, dtype, B, T, Hq, Hk) of the queries and keys, either of which may be None."""
+    if head_size < 1:
+        raise ValueError("head_size must be at least 1")
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q and k are both None")

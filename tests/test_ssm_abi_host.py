@@ -167,3 +167,5 @@ def test_binding_refuses_what_the_kernels_would_misread(S):
         S.wkv_scan_forward(x, x, torch.zeros(8, 16), torch.zeros(1, 4, 16), torch.zeros(1, 4, 16))
     with pytest.raises(ValueError, match="both None"):
         S.wkv_norm_rotate(None, None, head_size=8)
+    with pytest.raises(ValueError, match="head_size"):
+        S.wkv_norm_rotate(x, None, head_size=0)

@@ -147,3 +147,37 @@ def test_deterministic_whatever_the_workspace_holds(S):
         ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
         runs.append(S.wkv_norm_rotate_backward(q, None, gq, None, w, inv_freq=dev(freqs(64)), head_size=64, workspace=ws))
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][2], runs[1][2])
+
+
+@pytest.mark.parametrize("K,R,il", [(64, 64, False), (16, 10, True)])
+def test_what_shared_memory_held_before_stays_out(S, K, R, il):
+    """Tokens past the end of a CTA's share have no angles: what another kernel
+    left in shared memory there (NaN, from a scan of NaN) must not reach the
+    weight sums."""
+    nan = torch.full((8, 64, 4096), float("nan"), device="cuda")
+    bc = torch.full((8, 64, 16), float("nan"), device="cuda")
+    for _ in range(2):
+        S.wkv_scan_backward(nan, nan, nan[0, :1].expand(16, 4096).t().contiguous(), bc, bc, nan)
+    q = torch.randn(1, 301, 3 * K, device="cuda")
+    w = torch.ones(K, device="cuda")
+    gq, _, gw, _ = S.wkv_norm_rotate_backward(q, None, torch.randn_like(q), None, w, inv_freq=dev(freqs(R)), head_size=K,
+                                              interleaved=il)
+    assert torch.isfinite(gq).all() and torch.isfinite(gw).all()
+
+
+@pytest.mark.parametrize("il", [False, True])
+def test_entries_from_R_on_are_left_as_they_are(S, il):
+    """An infinite gradient of an entry that does not turn stays where it is
+    (after the norm's own sums: its row), and no other row sees it."""
+    K, R = 32, 16
+    q = torch.randn(1, 5, 2 * K, device="cuda")
+    g = torch.randn(1, 5, 2 * K, device="cuda")
+    g[0, 2, R + 3] = float("inf")
+    w = torch.ones(K, device="cuda")
+    gq, _, gw, _ = S.wkv_norm_rotate_backward(q, None, g, None, w, inv_freq=dev(freqs(R)), head_size=K, interleaved=il)
+    bad = torch.zeros(1, 5, 2, dtype=torch.bool, device="cuda")
+    bad[0, 2, 0] = True
+    assert torch.equal(~torch.isfinite(gq).view(1, 5, 2, K).all(-1), bad)
+    fine = torch.ones(K, dtype=torch.bool, device="cuda")
+    fine[R + 3] = False
+    assert torch.equal(torch.isfinite(gw), fine)

@@ -243,6 +243,21 @@ def test_state_in_place_and_pieces(S):
     assert torch.equal(torch.cat(parts, 1), y) and torch.equal(state, last)
 
 
+@pytest.mark.parametrize("B,T,C", [(1, 2000, 64), (3, 400, 72)])
+def test_state_in_place_of_a_cut_launch(S, B, T, C):
+    """final_state = init_state where the sequence is cut along T: every piece
+    reads the initial state, whatever piece is done first."""
+    i = draw("f32", (B, T), C, 16, 1, seed=10)
+    pos, kw, _ = operands(i)
+    from rwkv_wkv_linear_mix_b200 import wkv
+    assert wkv.lib().wkv_scan_forward_workspace_bytes(B, T, C, 16, 1) > 0
+    y, last = S.wkv_scan_forward(*pos, **kw, init_state=dev(i["h0"]))
+    for _ in range(5):
+        state = dev(i["h0"])
+        y2, last2 = S.wkv_scan_forward(*pos, **kw, init_state=state, final_state=state)
+        assert last2 is state and torch.equal(y2, y) and torch.equal(state, last)
+
+
 @pytest.mark.parametrize("B,T,C", [(1, 400, 64), (4, 90, 512)])
 def test_deterministic_whatever_the_buffers_hold(S, B, T, C):
     i = draw("bf16", (B, T), C, 16, 1, seed=5)
