@@ -74,11 +74,12 @@ __device__ __forceinline__ void conv_window(const E* x, const E* prev, int64_t t
 }
 
 // SLOTS: sequence b is slot b, tokens cu[b] .. cu[b+1] of the packed tensors,
-// and x_prev is the slots' state; its tokens are split over the nrun CTAs.
+// and x_prev is the slots' state (also `state`, to be written); its tokens are
+// split over the nrun CTAs.
 template <class E, int W, bool SILU, bool SLOTS>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restrict__ x, const float* __restrict__ weight,
                                                                 const float* __restrict__ bias,
-                                                                const E* __restrict__ x_prev, E* __restrict__ y, int64_t T,
+                                                                const E* x_prev, E* state, E* __restrict__ y, int64_t T,
                                                                 int64_t C, int ncb, int nrun, int64_t Lt,
                                                                 const int32_t* __restrict__ cu, int64_t n_tokens,
                                                                 unsigned* err) {
@@ -116,6 +117,22 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restr
   for (int j = 0; j < W; ++j) ld_param2<N>(weight + (int64_t)j * C + c, w[j], 0.f);
   ld_param2<N>(bias ? bias + c : nullptr, bi, 0.f);
   conv_window<E, W, N>(xs, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
+  if (SLOTS && run == 0) {
+    // the slot's new state, the last W-1 of the old one and its tokens: the
+    // first run alone reads the state, so it alone may write it
+    E* st = state + b * (W - 1) * C + c;
+    Pack<E, N> rows[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int64_t t = T - (W - 1) + j;
+      if (t >= 0)
+        rows[j].load(xs + t * C);
+      else
+        rows[j].load(st + (t + W - 1) * C);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) rows[j].store(st + j * C);
+  }
   while (true) {
     Pack<E, N> next[U];
     xp += U * C;
@@ -138,33 +155,6 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restr
 #pragma unroll
     for (int j = 0; j < U; ++j) raw[j] = next[j];
   }
-}
-
-// The slots' new states, once their outputs are written: the last W-1 of the
-// old state and the slot's tokens. A thread reads all of its rows first.
-template <class E, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_state_kernel(const E* __restrict__ x, E* __restrict__ state, int64_t S,
-                                                                  int64_t C, const int32_t* __restrict__ cu,
-                                                                  int64_t n_tokens) {
-  constexpr int N = kConvN<E>;
-  const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int64_t nv = C / N;
-  if (i >= S * nv) return;
-  const int64_t b = i / nv, c = (i - b * nv) * N;
-  const int64_t beg = cu[b], end = cu[b + 1];
-  if (end <= beg || beg < 0 || end > n_tokens) return;
-  E* st = state + b * (W - 1) * C + c;
-  Pack<E, N> rows[W - 1];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) {
-    const int64_t t = end - beg - (W - 1) + j;
-    if (t >= 0)
-      rows[j].load(x + (beg + t) * C + c);
-    else
-      rows[j].load(st + (t + W - 1) * C);
-  }
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) rows[j].store(st + j * C);
 }
 
 // One token per slot.
@@ -343,7 +333,7 @@ wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
   const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, 16, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, false> : conv_fwd_kernel<E, W, false, false>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
-      static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), static_cast<E*>(a.y), a.T, a.C, s.ncb,
+      static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), nullptr, static_cast<E*>(a.y), a.T, a.C, s.ncb,
       s.nrun, s.Lt, nullptr, 0, nullptr);
   return launched("conv forward kernel launch failed", why);
 }
@@ -353,12 +343,9 @@ wkv_status run_chunk(const ConvArgs& a, cudaStream_t st, unsigned* err, const ch
   const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, 16, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, true> : conv_fwd_kernel<E, W, false, true>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
-      static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.state), static_cast<E*>(a.y), 0, a.C, s.ncb,
-      s.nrun, 0, a.cu, a.n_tokens, err);
-  if (wkv_status e = launched("conv chunk step kernel launch failed", why)) return e;
-  conv_state_kernel<E, W><<<(unsigned)ceil_div(a.B * (a.C / kConvN<E>), kConvThreads), kConvThreads, 0, st>>>(
-      static_cast<const E*>(a.x), static_cast<E*>(a.state), a.B, a.C, a.cu, a.n_tokens);
-  return launched("conv state kernel launch failed", why);
+      static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.state), static_cast<E*>(a.state),
+      static_cast<E*>(a.y), 0, a.C, s.ncb, s.nrun, 0, a.cu, a.n_tokens, err);
+  return launched("conv chunk step kernel launch failed", why);
 }
 template <class E, int W>
 wkv_status run_decode(const ConvArgs& a, cudaStream_t st, const char** why) {
@@ -374,10 +361,10 @@ wkv_status run_bwd(const ConvArgs& a, cudaStream_t st, const char** why) {
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), static_cast<const E*>(a.gy),
       static_cast<E*>(a.gx), static_cast<E*>(a.gx_prev), a.part, a.B, a.T, a.C, s.ncb, s.nrun, s.Lt);
   if (wkv_status e = launched("conv backward kernel launch failed", why)) return e;
-  SumOutputs out{};
-  for (int j = 0; j < W; ++j) out.plane[j] = a.gweight + j * a.C;
-  out.plane[W] = a.gbias;
-  return launch_sum_rows(a.part, W + 1, a.B * s.nrun, a.C, out, st, why);
+  SumRows sums{};
+  sums.rows = a.B * s.nrun;
+  for (int j = 0; j <= W; ++j) sums.add(a.part + j * sums.rows * a.C, a.C, j < W ? a.gweight + j * a.C : a.gbias);
+  return launch_sum_rows(sums, st, why);
 }
 
 #define WKV_CONV_DISPATCH(CALL)                                                        \

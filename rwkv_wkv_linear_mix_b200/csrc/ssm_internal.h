@@ -10,14 +10,22 @@ namespace wkv {
 // Address of the current device's error word (capi.cu).
 wkv_status device_error_word(unsigned** out);
 
-// out[i][c] = sum over the rows of part[i][rows][cols], in a fixed order, for
-// each plane i that has an output.
-struct SumOutputs {
+// For each of up to kMost planes that has an output: out[c] = the sum of
+// part[rows][cols] over its rows, in a fixed order. One launch.
+struct SumRows {
   static constexpr int kMost = 5;
-  float* plane[kMost];
+  struct Plane {
+    const float* part;
+    int64_t cols;
+    float* out;
+  } plane[kMost];
+  int planes;
+  int64_t rows;
+  void add(const float* part, int64_t cols, float* out) {
+    if (out) plane[planes++] = {part, cols, out};
+  }
 };
-wkv_status launch_sum_rows(const float* part, int planes, int64_t rows, int64_t cols, const SumOutputs& out,
-                           cudaStream_t stream, const char** why);
+wkv_status launch_sum_rows(const SumRows& s, cudaStream_t stream, const char** why);
 
 // ---- short causal convolution ------------------------------------------------
 struct ConvArgs {

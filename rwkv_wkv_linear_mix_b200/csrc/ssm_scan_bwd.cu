@@ -486,9 +486,12 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
   scan_sum_bc_kernel<E><<<dim3((unsigned)ceil_div(n4, 256), 2), 256, 0, st>>>(b.part_bc, p.nbg, n4, static_cast<E*>(b.gB),
                                                                             static_cast<E*>(b.gC));
   if (wkv_status s = launched("scan gB, gC sum kernel launch failed", why)) return s;
-  const int64_t rows = a.B * cut.nseg;
-  if (wkv_status s = launch_sum_rows(b.part_a, 1, rows, a.C * a.N, SumOutputs{{b.gA}}, st, why)) return s;
-  return launch_sum_rows(b.part_d, 2, rows, a.C, SumOutputs{{b.gD, b.gdt_bias}}, st, why);
+  SumRows sums{};
+  sums.rows = a.B * cut.nseg;
+  sums.add(b.part_a, a.C * a.N, b.gA);
+  sums.add(b.part_d, a.C, b.gD);
+  sums.add(b.part_d + sums.rows * a.C, a.C, b.gdt_bias);
+  return launch_sum_rows(sums, st, why);
 }
 
 }  // namespace

@@ -182,51 +182,64 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
   }
 }
 
-// One token per slot: a stream of the states. The lanes of a channel pair
-// each work the token's step size out for themselves.
+// One token per slot: a stream of the states, 16 bytes per lane and channel.
+// The lanes of a channel pair each work the token's step size out for
+// themselves; a thread takes the same states of kDecodeSlots slots, so that
+// the loads of both are in flight together and A is read once.
 constexpr int kDecodeThreads = 128;
+constexpr int kDecodeSlots = 2;  // 1: 31, 2: 27, 4: 28 us for 256 slots, C=4096 N=16 bf16
 template <class E, int LPC, int S>
 __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanParams p) {
+  constexpr int U = kDecodeSlots;
   const int64_t i = (int64_t)blockIdx.x * kDecodeThreads + threadIdx.x;
-  const int64_t np = p.C / 2, all = p.B * np * LPC;
+  const int64_t np = p.C / 2, all = (p.B + U - 1) / U * np * LPC;
   const int g = (int)(i % LPC);
-  const int64_t k0 = min(i, all - 1) / LPC, s = k0 / np, c = (k0 - s * np) * 2;
-  const bool on = i < all && S * g < p.N;
+  const int64_t k0 = min(i, all - 1) / LPC, s0 = k0 / np * U, c = k0 % np * 2;
+  const bool state_on = i < all && S * g < p.N;
   const int64_t grp = c / p.Cg;
-  const float2 x = ld_pair(static_cast<const E*>(p.x) + s * p.C + c);
-  const float2 dt = ld_pair(static_cast<const E*>(p.dt) + s * p.C + c);
-  const float2 z = p.z ? ld_pair(static_cast<const E*>(p.z) + s * p.C + c) : splat2(0.f);
+  States<S> h[U];
+  float2 x[U], dt[U], z[U];
+  Pack<E, S> pb[U], pc[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t s = min(s0 + u, p.B - 1);
+    const bool on = state_on && s0 + u < p.B;
+    h[u] = ld_states_wide<S>(p.final_state + (s * p.C + c) * p.N + S * g, p.N, on);
+    x[u] = ld_pair(static_cast<const E*>(p.x) + s * p.C + c);
+    dt[u] = ld_pair(static_cast<const E*>(p.dt) + s * p.C + c);
+    z[u] = p.z ? ld_pair(static_cast<const E*>(p.z) + s * p.C + c) : splat2(0.f);
+    pb[u].zero();
+    pc[u].zero();
+    if (on) {
+      pb[u].load(static_cast<const E*>(p.Bm) + (s * p.G + grp) * p.N + S * g);
+      pc[u].load(static_cast<const E*>(p.Cm) + (s * p.G + grp) * p.N + S * g);
+    }
+  }
+  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, state_on), kLog2e);
   const float2 bias = p.dt_bias ? ld_pair(p.dt_bias + c) : splat2(0.f);
   const float2 D = p.D ? ld_pair(p.D + c) : splat2(0.f);
-  float Bf[S] = {}, Cf[S] = {};
-  if (on) {
-    Pack<E, S> pb, pc;
-    pb.load(static_cast<const E*>(p.Bm) + (s * p.G + grp) * p.N + S * g);
-    pc.load(static_cast<const E*>(p.Cm) + (s * p.G + grp) * p.N + S * g);
-    pb.get(Bf);
-    pc.get(Cf);
-  }
-  float* st = p.final_state + (s * p.C + c) * p.N + S * g;
-  States<S> h = ld_states_wide<S>(st, p.N, on);
-  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, on), kLog2e);
-  const float2 d = scan_step_size2(dt, bias, p.softplus);
-  Row<S> Bv, Cv;
 #pragma unroll
-  for (int n = 0; n < S; ++n) Bv.n[n] = Bf[n], Cv.n[n] = Cf[n];
-  scan_absorb(h, scan_decay(d, A2), mul2(d, x), Bv);
-  if (on) st_states_wide<S>(st, p.N, h, 0);
-  const float2 dot = scan_dot<S>(h, Cv);
-  float out[2] = {dot.x, dot.y};
-  // one lane bit at a time, as the walk's halving steps do
+  for (int u = 0; u < U; ++u) {
+    const bool there = i < all && s0 + u < p.B;
+    Row<S> Bv, Cv;
+    pb[u].get(Bv.n);
+    pc[u].get(Cv.n);
+    const float2 d = scan_step_size2(dt[u], bias, p.softplus);
+    scan_absorb(h[u], scan_decay(d, A2), mul2(d, x[u]), Bv);
+    if (state_on && there) st_states_wide<S>(p.final_state + ((s0 + u) * p.C + c) * p.N + S * g, p.N, h[u], 0);
+    const float2 dot = scan_dot<S>(h[u], Cv);
+    float out[2] = {dot.x, dot.y};
+    // one lane bit at a time, as the walk's halving steps do
 #pragma unroll
-  for (int m = 1; m < LPC; m *= 2) {
-    out[0] = __fadd_rn(out[0], __shfl_xor_sync(0xffffffffu, out[0], m));
-    out[1] = __fadd_rn(out[1], __shfl_xor_sync(0xffffffffu, out[1], m));
-  }
-  if (i < all && g == 0) {
-    const float2 gate = p.z ? mul2(z, sigmoid2(z)) : splat2(1.f), e = mul2(D, x);
-    st_pair(static_cast<E*>(p.y) + s * p.C + c,
-            make_float2(__fmul_rn(__fadd_rn(out[0], e.x), gate.x), __fmul_rn(__fadd_rn(out[1], e.y), gate.y)));
+    for (int m = 1; m < LPC; m *= 2) {
+      out[0] = __fadd_rn(out[0], __shfl_xor_sync(0xffffffffu, out[0], m));
+      out[1] = __fadd_rn(out[1], __shfl_xor_sync(0xffffffffu, out[1], m));
+    }
+    if (there && g == 0) {
+      const float2 gate = p.z ? mul2(z[u], sigmoid2(z[u])) : splat2(1.f), e = mul2(D, x[u]);
+      st_pair(static_cast<E*>(p.y) + (s0 + u) * p.C + c,
+              make_float2(__fmul_rn(__fadd_rn(out[0], e.x), gate.x), __fmul_rn(__fadd_rn(out[1], e.y), gate.y)));
+    }
   }
 }
 
@@ -283,7 +296,7 @@ template <class E, int LPC, int S>
 wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
   const ScanParams p = scan_params(a, ScanCut{1, 0});
   constexpr int DL = LPC * S / 4;  // a stream of states: 16 bytes per lane and channel
-  const int64_t threads = a.B * (a.C / 2) * DL;
+  const int64_t threads = ceil_div(a.B, kDecodeSlots) * (a.C / 2) * DL;
   scan_decode_kernel<E, DL, 4><<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
   return launched("scan decode kernel launch failed", why);
 }
