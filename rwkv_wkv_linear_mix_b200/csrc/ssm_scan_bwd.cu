@@ -35,11 +35,13 @@ template <class E, class Geo>
 struct ScanBwdShared {
   static constexpr int WARPS = Geo::THREADS / 32;
   ScanRaw<E, Geo, kActs> raw;                    // the tile that is next
-  float4 dd[kScanTile][Geo::HB][2];              // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
-  float2 gs[kScanTile][Geo::HB][2];              // gs0, gs1; and swapped
-  // per channel, to finish with: d, x, softplus'(raw), gy silu'(z) (rows a
-  // pair apart, since the lanes read 4 tokens at once)
-  float4 fin[kScanTile][Geo::HB + 1][2];
+  // per channel pair: d0, d1, d0 x0, d1 x1, and gs0, gs1; and with the channels
+  // swapped (64 bytes further on in the banks, so that a warp reads both
+  // orders at once)
+  float4 dd[kScanTile][2][Geo::HB + 4];
+  float2 gs[kScanTile][2][Geo::HB + 8];
+  // per channel, to finish with: d, x, softplus'(raw), gy silu'(z)
+  float4 fin[kScanTile][2][Geo::HB + 4];
   float B[kScanTile][Geo::S][Geo::NP];           // in each order of a lane's states
   float C[kScanTile][Geo::S][Geo::NP];
   float sum[2][WARPS][kScanTile][Geo::NP];       // gB, gC of each warp's channels
@@ -147,11 +149,12 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
         gz = mul2(gy, mul2(s, fma2(z, sub2(splat2(1.f), s), splat2(1.f))));
       }
       const float2 dx = mul2(d, x);
-      sm.dd[t][lp][0] = make_float4(d.x, d.y, dx.x, dx.y);
-      sm.dd[t][lp][1] = make_float4(d.y, d.x, dx.y, dx.x);
-      *reinterpret_cast<float4*>(sm.gs[t][lp]) = make_float4(gs.x, gs.y, gs.y, gs.x);
-      sm.fin[t][lp][0] = make_float4(d.x, x.x, sp.x, gz.x);
-      sm.fin[t][lp][1] = make_float4(d.y, x.y, sp.y, gz.y);
+      sm.dd[t][0][lp] = make_float4(d.x, d.y, dx.x, dx.y);
+      sm.dd[t][1][lp] = make_float4(d.y, d.x, dx.y, dx.x);
+      sm.gs[t][0][lp] = gs;
+      sm.gs[t][1][lp] = make_float2(gs.y, gs.x);
+      sm.fin[t][0][lp] = make_float4(d.x, x.x, sp.x, gz.x);
+      sm.fin[t][1][lp] = make_float4(d.y, x.y, sp.y, gz.y);
     }
   };
 
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
     // up to the last SUB tokens, leaving the states on the way
 #pragma unroll
     for (int t = 0; t < kScanTile - SUB; ++t) {
-      const float4 dd = sm.dd[t][pair][order.swap];
+      const float4 dd = sm.dd[t][order.swap][pair];
       scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[t][order.perm][S * g]));
       if ((t + 1) % SUB == 0 && t + 1 < kScanTile - SUB) st_h((t + 1) / SUB, h);
     }
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
       States<S> a[SUB], ah[SUB];
 #pragma unroll
       for (int t = 0; t < SUB; ++t) {
-        const float4 dd = sm.dd[tb + t][pair][order.swap];
+        const float4 dd = sm.dd[tb + t][order.swap][pair];
         const Row<S> Bv = ld_row<S>(&sm.B[tb + t][order.perm][S * g]);
         a[t] = scan_decay(make_float2(dd.x, dd.y), A2);
 #pragma unroll
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
 #pragma unroll
         for (int u = 1; u >= 0; --u) {
           const int tt = tb + t + u;
-          const float4 dd = sm.dd[tt][pair][order.swap];
-          const float2 gs = sm.gs[tt][pair][order.swap];
+          const float4 dd = sm.dd[tt][order.swap][pair];
+          const float2 gs = sm.gs[tt][order.swap][pair];
           const Row<S> Bv = ld_row<S>(&sm.B[tt][order.perm][S * g]), Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
           const float2 d = make_float2(dd.x, dd.y), dx = make_float2(dd.z, dd.w);
           States<S> Q, W, ht;
@@ -304,8 +307,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
 #pragma unroll
       for (int v = 0; v < kPairSums<LPC>; ++v) {
         const int tt = tb + pair_sum_first<LPC>(g) + v;
-        const float4 fin = sm.fin[tt][pair][order.swap];
-        const float d = fin.x, x = fin.y, gs = sm.gs[tt][pair][order.swap].x;
+        const float4 fin = sm.fin[tt][order.swap][pair];
+        const float d = fin.x, x = fin.y, gs = sm.gs[tt][order.swap][pair].x;
         const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gs, D));
         const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
         if (tt < left && ch_on && g < 8) {

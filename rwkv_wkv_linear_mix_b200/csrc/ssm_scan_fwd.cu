@@ -32,7 +32,9 @@ enum { kActX, kActDt, kActZ, kActs };
 template <class E, class Geo>
 struct ScanFwdShared {
   ScanRaw<E, Geo, kActs> raw[2];         // the tile at work, and the next in flight
-  float4 dd[kScanTile][Geo::HB][2];      // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
+  // per channel pair: d0, d1, d0 x0, d1 x1; and with the channels swapped
+  // (64 bytes further on in the banks, so that a warp reads both orders at once)
+  float4 dd[kScanTile][2][Geo::HB + 4];
   float B[kScanTile][Geo::NP];
   float C[kScanTile][Geo::NP];
 };
@@ -80,17 +82,17 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
   const float2 bias = p.dt_bias && 2 * lp < channels ? ld_pair(p.dt_bias + w.c0 + 2 * lp) : splat2(0.f);
   auto convert = [&](int i) {
     const ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
+    const int left = (int)min(tend - tbeg - (int64_t)i * kScanTile, (int64_t)kScanTile);
     r.template put_bc<1>(0, &sm.B[0][0]);
     if constexpr (MODE != kScanCarry) r.template put_bc<1>(1, &sm.C[0][0]);
-    const int left = (int)min(tend - tbeg - (int64_t)i * kScanTile, (int64_t)kScanTile);
 #pragma unroll
     for (int j = 0; j < Geo::PT; ++j) {
       const int t = tid / Geo::HB + j * Geo::ROWS;
       // a token past the end: d = 0 leaves the state as it is
       const float2 d = t < left ? scan_step_size2(ld_pair(&r.act[kActDt][t][2 * lp]), bias, p.softplus) : splat2(0.f);
       const float2 dx = mul2(d, ld_pair(&r.act[kActX][t][2 * lp]));
-      sm.dd[t][lp][0] = make_float4(d.x, d.y, dx.x, dx.y);
-      sm.dd[t][lp][1] = make_float4(d.y, d.x, dx.y, dx.x);
+      sm.dd[t][0][lp] = make_float4(d.x, d.y, dx.x, dx.y);
+      sm.dd[t][1][lp] = make_float4(d.y, d.x, dx.y, dx.x);
     }
   };
 
@@ -129,13 +131,14 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
       st_states_wide<S>(p.ckpt + ((w.b * nck + m) * p.C + c) * p.N + S * g, p.N, h, swap);
     }
     float2 tile_d = splat2(0.f);
+    const ScanRaw<E, Geo, kActs>& raw = sm.raw[i & 1];
     float done[kScanTile / 4][kPairSums<LPC>];  // stored after the walk: a store would hold back the loads behind it
 #pragma unroll
     for (int tg = 0; tg < kScanTile; tg += 4) {
       float2 dots[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 dd = sm.dd[tg + j][pair][swap];
+        const float4 dd = sm.dd[tg + j][swap][pair];
         const float2 d = make_float2(dd.x, dd.y);
         scan_absorb(h, scan_decay(d, A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[tg + j][S * g]));
         if constexpr (MODE != kScanCarry)
@@ -153,16 +156,15 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
     if (MODE != kScanCarry && p.y) {
       // done[tg / 4][v]: channel `swap` of token tg + out0 + v
       const int left = ch_on && g < 8 ? (int)min(tend - t0, (int64_t)kScanTile) : 0;
-      const ScanRaw<E, Geo, kActs>& r = sm.raw[i & 1];
       E* y = static_cast<E*>(p.y) + (first + t0) * p.C + c + swap;
 #pragma unroll
       for (int tg = 0; tg < kScanTile; tg += 4) {
 #pragma unroll
         for (int v = 0; v < kPairSums<LPC>; ++v) {
           const int t = tg + out0 + v;
-          float o = __fadd_rn(done[tg / 4][v], __fmul_rn(D, Elem<E>::to_f32(r.act[kActX][t][2 * pair + swap])));
+          float o = __fadd_rn(done[tg / 4][v], __fmul_rn(D, Elem<E>::to_f32(raw.act[kActX][t][2 * pair + swap])));
           if (p.z) {
-            const float z = Elem<E>::to_f32(r.act[kActZ][t][2 * pair + swap]);
+            const float z = Elem<E>::to_f32(raw.act[kActZ][t][2 * pair + swap]);
             o = __fmul_rn(o, __fmul_rn(z, sigmoid_f(z)));
           }
           if (t < left) y[t * (int)p.C] = Elem<E>::from_f32(o);
