@@ -39,9 +39,12 @@ struct ScanBwdShared {
   // swapped (64 bytes further on in the banks, so that a warp reads both
   // orders at once)
   float4 dd[kScanTile][2][Geo::HB + 4];
-  float2 gs[kScanTile][2][Geo::HB + 8];
-  // per channel, to finish with: d, x, softplus'(raw), gy silu'(z)
-  float4 fin[kScanTile][2][Geo::HB + 4];
+  float2 gs[kScanTile][2][Geo::HB + 10];
+  // per channel, to finish with: d, x, softplus'(raw), gy silu'(z); channel 1
+  // 64 bytes further on, the next token 16, since a lane group reads both
+  // channels of 4 tokens at once
+  static constexpr int FIN1 = Geo::HB + 4, FIN = 2 * FIN1 + 1;
+  float4 fin[kScanTile][FIN];
   float B[kScanTile][Geo::S][Geo::NP];           // in each order of a lane's states
   float C[kScanTile][Geo::S][Geo::NP];
   float sum[2][WARPS][kScanTile][Geo::NP];       // gB, gC of each warp's channels
@@ -153,8 +156,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
       sm.dd[t][1][lp] = make_float4(d.y, d.x, dx.y, dx.x);
       sm.gs[t][0][lp] = gs;
       sm.gs[t][1][lp] = make_float2(gs.y, gs.x);
-      sm.fin[t][0][lp] = make_float4(d.x, x.x, sp.x, gz.x);
-      sm.fin[t][1][lp] = make_float4(d.y, x.y, sp.y, gz.y);
+      sm.fin[t][lp] = make_float4(d.x, x.x, sp.x, gz.x);
+      sm.fin[t][Shared::FIN1 + lp] = make_float4(d.y, x.y, sp.y, gz.y);
     }
   };
 
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
 #pragma unroll
       for (int v = 0; v < kPairSums<LPC>; ++v) {
         const int tt = tb + pair_sum_first<LPC>(g) + v;
-        const float4 fin = sm.fin[tt][order.swap][pair];
+        const float4 fin = sm.fin[tt][order.swap * Shared::FIN1 + pair];
         const float d = fin.x, x = fin.y, gs = sm.gs[tt][order.swap][pair].x;
         const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gs, D));
         const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
