@@ -6,7 +6,8 @@
  * that hold here too (memory, layout, alignment, sizes, dtype, C granularity,
  * streams, errors, threads); the status, dtype and device-error codes are
  * those of wkv.h, and failures are read with wkv_last_error() and
- * wkv_device_error(). Outputs must not overlap inputs unless stated.
+ * wkv_device_error(). Outputs must not overlap inputs unless stated. The
+ * current device must be the tensors' device; C is at most 2^26.
  */
 #ifndef WKV_B200_SSM_H
 #define WKV_B200_SSM_H
