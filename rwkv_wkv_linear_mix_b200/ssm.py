@@ -76,13 +76,25 @@ def _may(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
     return None if t is None else _has(t, name, dtype, shape, dev)
 
 
-def _first(t: torch.Tensor, name: str, dims: int) -> torch.device:
-    """Checks the tensor that the sizes are taken from."""
-    _want(t, name)
+_CODES = {torch.float32: _wkv.WKV_F32, torch.bfloat16: _wkv.WKV_BF16}
+
+
+def _first(t: torch.Tensor, name: str, dims: int):
+    """(device, dtype code) of the tensor that the sizes are taken from."""
+    if not (t.is_cuda and t.is_contiguous()):
+        _want(t, name)
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    _dtype_code(t)
-    return t.device
+    code = _CODES.get(t.dtype)
+    return t.device, _dtype_code(t) if code is None else code
+
+
+def _like(t: Optional[torch.Tensor], given: Optional[torch.Tensor], name: str, dtype, shape, dev):
+    """(tensor, address) of an output: the one given, checked, or a new one like `t`."""
+    if given is None:
+        given = torch.empty_like(t)
+        return given, given.data_ptr()
+    return given, _has(given, name, dtype, shape, dev)
 
 
 def _space(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
@@ -113,13 +125,13 @@ def wkv_conv_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     weight: [W, C] float32 (W 2..4, the last row meets the current token);
     bias: [C] float32; x_prev: [B, W-1, C], the tokens before x (None: zeros).
     Returns y like x, put through silu unless ``silu`` is false."""
-    dev = _first(x, "x", 3)
+    dev, code = _first(x, "x", 3)
     B, T, C = x.shape
     W, f32 = _taps(weight, C), torch.float32
-    y = torch.empty_like(x) if y is None else y
-    _call("wkv_conv_forward", dev, B, T, C, _dtype_code(x), W, int(silu), x.data_ptr(),
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
+    _call("wkv_conv_forward", dev, B, T, C, code, W, int(silu), x.data_ptr(),
           _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
-          _may(x_prev, "x_prev", x.dtype, (B, W - 1, C), dev), _has(y, "y", x.dtype, x.shape, dev))
+          _may(x_prev, "x_prev", x.dtype, (B, W - 1, C), dev), yp)
     return y
 
 
@@ -128,22 +140,22 @@ def wkv_conv_backward(x, weight, gy, bias=None, x_prev=None, *, silu: bool = Tru
     """Gradients of sum(gy * wkv_conv_forward(x, weight, bias, x_prev)).
     Returns (gx, gweight, gbias, gx_prev); gbias is None without a bias,
     gx_prev unless wanted (or a buffer is passed)."""
-    dev = _first(x, "x", 3)
+    dev, code = _first(x, "x", 3)
     B, T, C = x.shape
-    W, f32 = _taps(weight, C), torch.float32
-    gx = torch.empty_like(x) if gx is None else gx
-    gweight = torch.empty_like(weight) if gweight is None else gweight
-    if gbias is None and bias is not None:
-        gbias = torch.empty_like(bias)
+    W, f32, e = _taps(weight, C), torch.float32, x.dtype
+    wp = _has(weight, "weight", f32, (W, C), dev)
+    bp = _may(bias, "bias", f32, (C,), dev)
+    gx, gxp = _like(x, gx, "gx", e, x.shape, dev)
+    gweight, gwp = _like(weight, gweight, "gweight", f32, (W, C), dev)
+    gbp = None
+    if bias is not None or gbias is not None:
+        gbias, gbp = _like(bias, gbias, "gbias", f32, (C,), dev)
     if gx_prev is None and want_gx_prev:
-        gx_prev = torch.empty((B, W - 1, C), dtype=x.dtype, device=dev)
-    code = _dtype_code(x)
-    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_conv_backward_workspace_bytes(B, T, C, code, W)), dev)
-    _call("wkv_conv_backward", dev, B, T, C, code, W, int(silu), x.data_ptr(),
-          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
-          _may(x_prev, "x_prev", x.dtype, (B, W - 1, C), dev), _has(gy, "gy", x.dtype, x.shape, dev),
-          _has(gx, "gx", x.dtype, x.shape, dev), _has(gweight, "gweight", f32, (W, C), dev),
-          _may(gbias, "gbias", f32, (C,), dev), _may(gx_prev, "gx_prev", x.dtype, (B, W - 1, C), dev), ptr, nbytes)
+        gx_prev = torch.empty((B, W - 1, C), dtype=e, device=dev)
+    ptr, nbytes, workspace = _space(workspace, _fn["wkv_conv_backward_workspace_bytes"](B, T, C, code, W), dev)
+    _call("wkv_conv_backward", dev, B, T, C, code, W, int(silu), x.data_ptr(), wp, bp,
+          _may(x_prev, "x_prev", e, (B, W - 1, C), dev), _has(gy, "gy", e, x.shape, dev), gxp, gwp, gbp,
+          _may(gx_prev, "gx_prev", e, (B, W - 1, C), dev), ptr, nbytes)
     return gx, gweight, gbias, gx_prev
 
 
@@ -152,26 +164,24 @@ def wkv_conv_chunk_step(x, weight, cu_tokens: torch.Tensor, state: torch.Tensor,
     """The convolution over slots. x: [n, C], the tokens of all slots packed;
     cu_tokens: int32 [S+1] on the device; state: [S, W-1, C] like x, the last
     tokens of each slot, read and written in place. Returns y like x."""
-    dev = _first(x, "x", 2)
+    dev, code = _first(x, "x", 2)
     n, C = x.shape
     W, S, f32 = _taps(weight, C), state.shape[0], torch.float32
-    y = torch.empty_like(x) if y is None else y
-    _call("wkv_conv_chunk_step", dev, S, C, _dtype_code(x), W, int(silu), x.data_ptr(),
-          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
-          _has(y, "y", x.dtype, x.shape, dev), n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
+    _call("wkv_conv_chunk_step", dev, S, C, code, W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp, n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
           _has(state, "state", x.dtype, (S, W - 1, C), dev))
     return y
 
 
 def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: bool = True, y=None) -> torch.Tensor:
     """One token for every slot: x, y [S, C]; state as for wkv_conv_chunk_step."""
-    dev = _first(x, "x", 2)
+    dev, code = _first(x, "x", 2)
     S, C = x.shape
     W, f32 = _taps(weight, C), torch.float32
-    y = torch.empty_like(x) if y is None else y
-    _call("wkv_conv_decode_step", dev, S, C, _dtype_code(x), W, int(silu), x.data_ptr(),
-          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev),
-          _has(y, "y", x.dtype, x.shape, dev), _has(state, "state", x.dtype, (S, W - 1, C), dev))
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
+    _call("wkv_conv_decode_step", dev, S, C, code, W, int(silu), x.data_ptr(),
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp, _has(state, "state", x.dtype, (S, W - 1, C), dev))
     return y
 
 
@@ -179,33 +189,37 @@ def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: boo
 # per-head norm with position rotation
 # ----------------------------------------------------------------------------
 
-def _heads(q, k, head_size):
-    """(device, dtype, B, T, Hq, Hk) of the queries and keys, either of which may be None."""
-    if head_size < 1:
+def _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, K):
+    """(device, dtype, dtype code, sizes B T Hq Hk K R, the addresses of the
+    operands) of a call; q or k may be None."""
+    if K < 1:
         raise ValueError("head_size must be at least 1")
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q and k are both None")
-    dev = _first(lead, "q" if q is not None else "k", 3)
-    B, T, _ = lead.shape
-    heads = []
-    for name, t in (("q", q), ("k", k)):
-        if t is None:
-            heads.append(0)
-            continue
-        if t.dim() != 3 or t.shape[2] % head_size:
-            raise ValueError(f"{name} must be [B, T, H * {head_size}], got {tuple(t.shape)}")
-        _has(t, name, lead.dtype, (B, T, t.shape[2]), dev)
-        heads.append(t.shape[2] // head_size)
-    return dev, lead.dtype, B, T, heads[0], heads[1]
-
-
-def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, K, dev):
-    f32 = torch.float32
+    dev, code = _first(lead, "q" if q is not None else "k", 3)
+    B, T, width = lead.shape
+    e, f32 = lead.dtype, torch.float32
+    qp = kp = None
+    Hq = Hk = 0
+    if q is not None:
+        Hq, odd = divmod(width, K)
+        qp = q.data_ptr()
+    else:
+        Hk, odd = divmod(width, K)
+        kp = k.data_ptr()
+    if q is not None and k is not None:
+        if k.dim() != 3:
+            raise ValueError(f"k must have 3 dimensions, got shape {tuple(k.shape)}")
+        Hk, more = divmod(k.shape[2], K)
+        odd = odd or more
+        kp = _has(k, "k", e, (B, T, k.shape[2]), dev)
+    if odd:
+        raise ValueError(f"q and k must be [B, T, H * {K}]")
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return R, (_may(q_weight, "q_weight", f32, (K,), dev), _may(k_weight, "k_weight", f32, (K,), dev),
-               _may(inv_freq, "inv_freq", f32, (R // 2,), dev),
-               _may(positions, "positions", torch.int32, (B, T), dev))
+    return dev, e, code, (B, T, Hq, Hk, K, R), (
+        qp, kp, _may(q_weight, "q_weight", f32, (K,), dev), _may(k_weight, "k_weight", f32, (K,), dev),
+        _may(inv_freq, "inv_freq", f32, (R // 2,), dev), _may(positions, "positions", torch.int32, (B, T), dev))
 
 
 def wkv_norm_rotate(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, *, head_size: int,
@@ -215,18 +229,14 @@ def wkv_norm_rotate(q, k, q_weight=None, k_weight=None, inv_freq=None, positions
     [B, T, Hk*K] (either may be None); q_weight, k_weight: [K] float32;
     inv_freq: [R/2] float32 (None: no rotation); positions: int32 [B, T] (None:
     pos_offset + t). q_out=q and k_out=k work in place. Returns (q_out, k_out)."""
-    dev, dtype, B, T, Hq, Hk = _heads(q, k, head_size)
-    R, (wq, wk, fr, po) = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, head_size, dev)
-    outs = []
-    for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-        o = torch.empty_like(t) if t is not None and o is None else o
-        if t is not None:
-            _has(o, name, dtype, t.shape, dev)
-        outs.append(o if t is not None else None)
-    p = [None if t is None else t.data_ptr() for t in (q, k, outs[0], outs[1])]
-    _call("wkv_norm_rotate", dev, B, T, Hq, Hk, head_size, R, _dtype_code(q if q is not None else k), p[0], p[1], wq, wk,
-          eps, fr, po, pos_offset, int(interleaved), p[2], p[3])
-    return outs[0], outs[1]
+    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, head_size)
+    qo = ko = None
+    if q is not None:
+        q_out, qo = _like(q, q_out, "q_out", e, q.shape, dev)
+    if k is not None:
+        k_out, ko = _like(k, k_out, "k_out", e, k.shape, dev)
+    _call("wkv_norm_rotate", dev, *sizes, code, qp, kp, wq, wk, eps, fr, po, pos_offset, int(interleaved), qo, ko)
+    return q_out if q is not None else None, k_out if k is not None else None
 
 
 def wkv_norm_rotate_backward(q, k, gq_out, gk_out, q_weight=None, k_weight=None, inv_freq=None, positions=None, *,
@@ -235,23 +245,24 @@ def wkv_norm_rotate_backward(q, k, gq_out, gk_out, q_weight=None, k_weight=None,
     """Gradients of sum(gq_out * q_out) + sum(gk_out * k_out) for wkv_norm_rotate
     with the same arguments. Returns (gq, gk, gq_weight, gk_weight); a weight's
     gradient is None where there is no such weight."""
-    dev, dtype, B, T, Hq, Hk = _heads(q, k, head_size)
-    K = head_size
-    R, (wq, wk, fr, po) = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, B, T, K, dev)
-    grads, weights = [], []
-    for name, t, go, g, w in (("q", q, gq_out, gq, q_weight), ("k", k, gk_out, gk, k_weight)):
-        if t is not None:
-            g = torch.empty_like(t) if g is None else g
-            _has(go, f"g{name}_out", dtype, t.shape, dev)
-            _has(g, f"g{name}", dtype, t.shape, dev)
-        grads.append(g if t is not None else None)
-        weights.append(None if w is None else torch.empty_like(w))
-    p = [None if t is None else t.data_ptr() for t in
-         (q, k, gq_out if q is not None else None, gk_out if k is not None else None, *grads, *weights)]
-    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, K)), dev)
-    _call("wkv_norm_rotate_backward", dev, B, T, Hq, Hk, K, R, _dtype_code(q if q is not None else k), *p[:4], wq, wk,
-          eps, fr, po, pos_offset, int(interleaved), *p[4:], ptr, nbytes)
-    return (*grads, *weights)
+    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, head_size)
+    gop = kop = gqp = gkp = gwqp = gwkp = gwq = gwk = None
+    if q is not None:
+        gop = _has(gq_out, "gq_out", e, q.shape, dev)
+        gq, gqp = _like(q, gq, "gq", e, q.shape, dev)
+    if k is not None:
+        kop = _has(gk_out, "gk_out", e, k.shape, dev)
+        gk, gkp = _like(k, gk, "gk", e, k.shape, dev)
+    if q_weight is not None:
+        gwq = torch.empty_like(q_weight)
+        gwqp = gwq.data_ptr()
+    if k_weight is not None:
+        gwk = torch.empty_like(k_weight)
+        gwkp = gwk.data_ptr()
+    ptr, nbytes, workspace = _space(workspace, _fn["wkv_norm_rotate_backward_workspace_bytes"](*sizes[:5]), dev)
+    _call("wkv_norm_rotate_backward", dev, *sizes, code, qp, kp, gop, kop, wq, wk, eps, fr, po, pos_offset,
+          int(interleaved), gqp, gkp, gwqp, gwkp, ptr, nbytes)
+    return gq if q is not None else None, gk if k is not None else None, gwq, gwk
 
 
 # ----------------------------------------------------------------------------
@@ -263,8 +274,8 @@ def scan_ckpt_shape(B: int, T: int, C: int, N: int):
 
 
 def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dims):
-    """(device, sizes, addresses of the operands) of a scan over x of `dims` dimensions."""
-    dev = _first(x, "x", dims)
+    """(device, dtype code, sizes, addresses of the operands) of a scan over x of `dims` dimensions."""
+    dev, code = _first(x, "x", dims)
     lead, C = tuple(x.shape[:-1]), x.shape[-1]
     if A.dim() != 2 or A.shape[0] != C:
         raise ValueError(f"A must be [C, N] with C = {C}, got {tuple(A.shape)}")
@@ -272,7 +283,7 @@ def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dims):
     if Bm.dim() != dims or N == 0 or Bm.shape[-1] % N:
         raise ValueError(f"Bm must be [..., G * N] with N = {N}, got {tuple(Bm.shape)}")
     G, bc = Bm.shape[-1] // N, (*lead, Bm.shape[-1])
-    return dev, lead, C, N, G, (
+    return dev, code, lead, C, N, G, (
         x.data_ptr(), _has(dt, "dt", e, x.shape, dev), _has(A, "A", f32, (C, N), dev), _has(Bm, "Bm", e, bc, dev),
         _has(Cm, "Cm", e, bc, dev), _may(D, "D", f32, (C,), dev), _may(z, "z", e, x.shape, dev),
         _may(dt_bias, "dt_bias", f32, (C,), dev))
@@ -285,16 +296,16 @@ def wkv_scan_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state=
     G*N]; D, dt_bias: [C] float32; init_state: [B, C, N] float32.
     Returns (y, final_state or None), or (y, final_state or None, ckpt) when
     ``want_ckpt`` (or a ckpt buffer is passed)."""
-    dev, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    dev, code, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
     f32 = torch.float32
-    y = torch.empty_like(x) if y is None else y
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
     if final_state is None and want_final_state:
         final_state = torch.empty((B, C, N), dtype=f32, device=dev)
     if ckpt is None and want_ckpt:
         ckpt = torch.empty(scan_ckpt_shape(B, T, C, N), dtype=f32, device=dev)
-    ptr, nbytes, workspace = _space(workspace, int(_lib.wkv_scan_forward_workspace_bytes(B, T, C, N, G)), dev)
-    _call("wkv_scan_forward", dev, B, T, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
-          _may(init_state, "init_state", f32, (B, C, N), dev), _has(y, "y", x.dtype, x.shape, dev),
+    ptr, nbytes, workspace = _space(workspace, _fn["wkv_scan_forward_workspace_bytes"](B, T, C, N, G), dev)
+    _call("wkv_scan_forward", dev, B, T, C, N, G, code, *ptrs, int(dt_softplus),
+          _may(init_state, "init_state", f32, (B, C, N), dev), yp,
           _may(final_state, "final_state", f32, (B, C, N), dev),
           _may(ckpt, "ckpt", f32, scan_ckpt_shape(B, T, C, N), dev), ptr, nbytes)
     return (y, final_state) if ckpt is None else (y, final_state, ckpt)
@@ -308,25 +319,25 @@ def wkv_scan_backward(x, dt, A, Bm, Cm, gy, D=None, z=None, dt_bias=None, init_s
     (None: regenerated). Returns (gx, gdt, gA, gB, gC, gD, gz, gdt_bias,
     g_init); the gradient of an operand that is None is None, and so is g_init
     unless wanted."""
-    dev, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    dev, code, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
     f32, e = torch.float32, x.dtype
-    gx = torch.empty_like(x) if gx is None else gx
-    gdt = torch.empty_like(x) if gdt is None else gdt
+    gx, gxp = _like(x, gx, "gx", e, x.shape, dev)
+    gdt, gdtp = _like(x, gdt, "gdt", e, x.shape, dev)
+    gzp = None
     if z is None:
         gz = None
-    elif gz is None:
-        gz = torch.empty_like(x)
+    else:
+        gz, gzp = _like(z, gz, "gz", e, x.shape, dev)
     gA, gB, gC = torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(Cm)
     gD = None if D is None else torch.empty_like(D)
     gbias = None if dt_bias is None else torch.empty_like(dt_bias)
     g_init = torch.empty((B, C, N), dtype=f32, device=dev) if want_g_init else None
-    need = int(_lib.wkv_scan_backward_workspace_bytes(B, T, C, N, G, int(ckpt is not None)))
-    ptr, nbytes, workspace = _space(workspace, need, dev)
-    _call("wkv_scan_backward", dev, B, T, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
+    ptr, nbytes, workspace = _space(
+        workspace, _fn["wkv_scan_backward_workspace_bytes"](B, T, C, N, G, int(ckpt is not None)), dev)
+    _call("wkv_scan_backward", dev, B, T, C, N, G, code, *ptrs, int(dt_softplus),
           _may(init_state, "init_state", f32, (B, C, N), dev), _has(gy, "gy", e, x.shape, dev),
           _may(g_final, "g_final", f32, (B, C, N), dev), _may(ckpt, "ckpt", f32, scan_ckpt_shape(B, T, C, N), dev),
-          _has(gx, "gx", e, x.shape, dev), _has(gdt, "gdt", e, x.shape, dev), gA.data_ptr(), gB.data_ptr(), gC.data_ptr(),
-          None if gD is None else gD.data_ptr(), _may(gz, "gz", e, x.shape, dev),
+          gxp, gdtp, gA.data_ptr(), gB.data_ptr(), gC.data_ptr(), None if gD is None else gD.data_ptr(), gzp,
           None if gbias is None else gbias.data_ptr(), None if g_init is None else g_init.data_ptr(), ptr, nbytes)
     return gx, gdt, gA, gB, gC, gD, gz, gbias, g_init
 
@@ -336,11 +347,10 @@ def wkv_scan_chunk_step(x, dt, A, Bm, Cm, cu_tokens: torch.Tensor, state: torch.
     """The scan over slots. x, dt, z: [n, C], Bm, Cm: [n, G*N], the tokens of all
     slots packed; cu_tokens: int32 [S+1] on the device; state: [S, C, N]
     float32, read and written in place. Returns y like x."""
-    dev, (n,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    dev, code, (n,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
     S = state.shape[0]
-    y = torch.empty_like(x) if y is None else y
-    _call("wkv_scan_chunk_step", dev, S, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
-          _has(y, "y", x.dtype, x.shape, dev), n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
+    _call("wkv_scan_chunk_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp, n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
           _has(state, "state", torch.float32, (S, C, N), dev))
     return y
 
@@ -349,8 +359,7 @@ def wkv_scan_decode_step(x, dt, A, Bm, Cm, state: torch.Tensor, D=None, z=None, 
                          dt_softplus: bool = True, y=None) -> torch.Tensor:
     """One token for every slot: x, dt, z, y [S, C], Bm, Cm [S, G*N]; state as for
     wkv_scan_chunk_step."""
-    dev, (S,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
-    y = torch.empty_like(x) if y is None else y
-    _call("wkv_scan_decode_step", dev, S, C, N, G, _dtype_code(x), *ptrs, int(dt_softplus),
-          _has(y, "y", x.dtype, x.shape, dev), _has(state, "state", torch.float32, (S, C, N), dev))
+    dev, code, (S,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
+    _call("wkv_scan_decode_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp, _has(state, "state", torch.float32, (S, C, N), dev))
     return y
