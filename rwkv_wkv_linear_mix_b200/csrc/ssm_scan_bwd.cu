@@ -173,8 +173,9 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
   const float D = p.D && ch_on ? p.D[c + order.swap] : 0.f;
   {
     const float* sums = p.carry + p.B * p.nseg * p.C * p.N;
-    for (int j = p.nseg - 1; j > w.seg; --j) {
-      if (on) {
+    if (on) {
+#pragma unroll 8
+      for (int j = p.nseg - 1; j > w.seg; --j) {
         const int64_t row = (w.b * p.nseg + j) * p.C + c;
         const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
         scan_fold(q, scan_decay(make_float2(sums[row + order.swap], sums[row + 1 - order.swap]), A2), s);

@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
   States<S> h = ld_states<S>(p.init_state + state_at, p.N, MODE != kScanCarry && on && p.init_state, order);
   if constexpr (MODE == kScanMain) {
     const float* sums = p.carry + p.B * p.nseg * p.C * p.N;
-    for (int j = 0; j < w.seg; ++j) {
-      if (on) {
+    if (on) {
+#pragma unroll 8
+      for (int j = 0; j < w.seg; ++j) {
         const int64_t row = (w.b * p.nseg + j) * p.C + c;
         const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
         scan_fold(h, scan_decay(make_float2(sums[row + swap], sums[row + 1 - swap]), A2), s);

@@ -126,3 +126,51 @@ def test_norm_rotate_ahead_of_the_head_state_recurrence(S, O, oracle):
     o, _ = wkv.wkv6_forward(rr, kk, v, w, u)
     want, _ = oracle.wkv6_forward(host64(rr), host64(kk), host64(v), host64(w), host64(u).reshape(H, K))
     assert rel_err(host64(o), want) < 2e-2
+
+
+def test_slots_and_single_tokens_in_a_graph(S):
+    """A captured step over slots and one of single tokens, replayed: each
+    replay moves the states on as an eager call does."""
+    i = draw()
+    t = {n: dev(a) for n, a in i.items()}
+    n = 7
+    tok = {k: t[k][:, :n].reshape(B * n, -1).contiguous() for k in ("u", "dt", "z", "Bm", "Cm")}
+    one = {k: t[k][:, n].contiguous() for k in ("u", "dt", "z", "Bm", "Cm")}
+    cu, kw = (n * torch.arange(B + 1, dtype=torch.int32)).cuda(), dict(D=t["D"], dt_bias=t["dt_bias"])
+
+    def step(conv, state):
+        x = S.wkv_conv_chunk_step(tok["u"], t["w"], cu, conv, t["bias"])
+        a = S.wkv_scan_chunk_step(x, tok["dt"], t["A"], tok["Bm"], tok["Cm"], cu, state, z=tok["z"], **kw)
+        x = S.wkv_conv_decode_step(one["u"], t["w"], conv, t["bias"])
+        return a, S.wkv_scan_decode_step(x, one["dt"], t["A"], one["Bm"], one["Cm"], state, z=one["z"], **kw)
+
+    conv, state = torch.zeros(B, W - 1, C, device="cuda"), torch.zeros(B, C, N, device="cuda")
+    want = [step(conv, state) for _ in range(3)]
+    conv2, state2 = torch.zeros_like(conv), torch.zeros_like(state)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(conv2, state2)
+    assert not conv2.any() and not state2.any()
+    for a, b in want:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], a) and torch.equal(got[1], b)
+    assert torch.equal(conv, conv2) and torch.equal(state, state2) and S.device_error() == 0
+
+
+def test_two_streams_at_once(S):
+    """The same calls on two streams together give what they give alone."""
+    i = draw()
+    t = {n: dev(a) for n, a in i.items()}
+    data, kw = (t["u"], t["dt"], t["A"], t["Bm"], t["Cm"]), dict(D=t["D"], z=t["z"], dt_bias=t["dt_bias"])
+    alone = [S.wkv_scan_backward(*data, t["gy"], **kw), S.wkv_conv_backward(t["u"], t["w"], t["gy"], t["bias"])]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append([S.wkv_scan_backward(*data, t["gy"], **kw), S.wkv_conv_backward(t["u"], t["w"], t["gy"], t["bias"])])
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, b in zip(alone, o):
+            assert all(p is None and q is None or torch.equal(p, q) for p, q in zip(a, b))
