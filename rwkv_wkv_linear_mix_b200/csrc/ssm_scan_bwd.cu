@@ -504,9 +504,6 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
 }  // namespace
 
 wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const char** why) {
-#ifdef WKV_QUICK
-  return run_backward<__nv_bfloat16, 8, 2>(a, stream, why);
-#else
   const bool bf = a.f.dtype == WKV_BF16;
   switch (scan_padded_states(a.f.N)) {
     case 8: return bf ? run_backward<__nv_bfloat16, 4, 2>(a, stream, why) : run_backward<float, 4, 2>(a, stream, why);
@@ -514,7 +511,6 @@ wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const
     case 32: return bf ? run_backward<__nv_bfloat16, 8, 4>(a, stream, why) : run_backward<float, 8, 4>(a, stream, why);
     default: return bf ? run_backward<__nv_bfloat16, 16, 4>(a, stream, why) : run_backward<float, 16, 4>(a, stream, why);
   }
-#endif
 }
 
 }  // namespace wkv

@@ -308,9 +308,6 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
 // four (half the lanes) a launch has half the warps, and what it saves in
 // lane exchanges it loses in waiting: 411 against 380 us at B=8 T=2048 C=2560
 // N=16, the same where there are channels enough.
-#ifdef WKV_QUICK
-#define WKV_SCAN_DISPATCH(CALL) return CALL(__nv_bfloat16, 8, 2);
-#else
 #define WKV_SCAN_DISPATCH(CALL)                                                   \
   const bool bf = a.dtype == WKV_BF16;                                            \
   switch (scan_padded_states(a.N)) {                                              \
@@ -319,7 +316,6 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
     case 32: return bf ? CALL(__nv_bfloat16, 8, 4) : CALL(float, 8, 4);           \
     default: return bf ? CALL(__nv_bfloat16, 16, 4) : CALL(float, 16, 4);         \
   }
-#endif
 
 // Pieces along T: none where the channels alone give two CTAs per SM, since
 // the carry pass costs most of a second walk (B=2 C=4096, 256 CTAs, cut and
