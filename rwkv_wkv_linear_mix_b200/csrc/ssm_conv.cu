@@ -20,9 +20,11 @@ namespace wkv {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvU = 4;      // tokens whose loads are issued together, one batch ahead (forward)
-constexpr int kConvBwdU = 4;  // (backward)
-constexpr int kConvBwdN = 4;        // channels per thread of the backward
+constexpr int kConvU = 4;        // tokens whose loads are issued together, one batch ahead (forward)
+constexpr int kConvBwdU = 4;     // (backward)
+constexpr int kConvBwdN = 4;     // channels per thread of the backward
+constexpr int kConvMinRun = 16;  // tokens of a run of the forward (its last of a sequence may be shorter)
+static_assert(kConvMinRun >= 3, "only the first run may look before the sequence");
 template <class E>
 constexpr int kConvN = 16 / (int)sizeof(E);  // channels per thread elsewhere
 
@@ -75,7 +77,8 @@ __device__ __forceinline__ void conv_window(const E* x, const E* prev, int64_t t
 
 // SLOTS: sequence b is slot b, tokens cu[b] .. cu[b+1] of the packed tensors,
 // and x_prev is the slots' state (also `state`, to be written); its tokens are
-// split over the nrun CTAs.
+// split over the nrun CTAs,
+// kConvMinRun tokens or more to each.
 template <class E, int W, bool SILU, bool SLOTS>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restrict__ x, const float* __restrict__ weight,
                                                                 const float* __restrict__ bias,
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restr
     }
     first = beg;
     T = end - beg;
-    Lt = (T + nrun - 1) / nrun;
+    Lt = max((T + nrun - 1) / nrun, (int64_t)kConvMinRun);
   }
   const int64_t t0 = run * Lt;
   if (t0 >= T) return;
@@ -119,7 +122,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const E* __restr
   conv_window<E, W, N>(xs, x_prev ? x_prev + b * (W - 1) * C + c : nullptr, t0, C, win);
   if (SLOTS && run == 0) {
     // the slot's new state, the last W-1 of the old one and its tokens: the
-    // first run alone reads the state, so it alone may write it
+    // first run alone reads the state (a run has at least W-1 tokens before
+    // it), so it may write it while others are at work
     E* st = state + b * (W - 1) * C + c;
     Pack<E, N> rows[W - 1];
 #pragma unroll
@@ -330,7 +334,7 @@ wkv_status launched(const char* what, const char** why) {
 
 template <class E, int W>
 wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
-  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, 16, 16);
+  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, kConvMinRun, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, false> : conv_fwd_kernel<E, W, false, false>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), nullptr, static_cast<E*>(a.y), a.T, a.C, s.ncb,
@@ -340,7 +344,7 @@ wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
 template <class E, int W>
 wkv_status run_chunk(const ConvArgs& a, cudaStream_t st, unsigned* err, const char** why) {
   // the lengths are on the device: the runs are cut for the mean length
-  const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, 16, 16);
+  const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, kConvMinRun, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, true> : conv_fwd_kernel<E, W, false, true>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.state), static_cast<E*>(a.state),

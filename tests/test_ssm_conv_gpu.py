@@ -113,6 +113,29 @@ def test_slots_match_forward_bit_for_bit(S, dtype, W):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("W", [2, 3, 4])
+def test_short_slots_among_long_ones(S, dtype, W):
+    """Slots of a few tokens in a batch whose mean length is hundreds: the bits
+    of one forward per slot, call after call."""
+    C, lengths = 72, [700, 1, 2, 900, 3, 4, 5, 0, 6, 7, 1500, 8, 9, 17]
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
+    n, slots = int(cu[-1]), len(lengths)
+    i = draw(dtype, W, C, 21, x=(n, C), st=(slots, W - 1, C))
+    x, w, b, start = dev(i["x"]), dev(i["w"]), dev(i["b"]), dev(i["st"])
+    want, after = torch.empty_like(x), start.clone()
+    for s, m in enumerate(lengths):
+        if m:
+            piece = x[cu[s]:cu[s + 1]]
+            want[cu[s]:cu[s + 1]] = S.wkv_conv_forward(piece[None].contiguous(), w, b, start[s:s + 1].contiguous())[0]
+            after[s] = torch.cat([start[s], piece])[-(W - 1):]
+    for _ in range(20):
+        state = start.clone()
+        y = S.wkv_conv_chunk_step(x, w, cu.cuda(), state, b)
+        assert torch.equal(y, want) and torch.equal(state, after)
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 3, 4])
 @pytest.mark.parametrize("slots", [1, 37])
 def test_decode_matches_slots_bit_for_bit(S, dtype, W, slots):
     C = 264
