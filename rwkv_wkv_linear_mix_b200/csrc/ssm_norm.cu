@@ -201,14 +201,16 @@ __device__ __forceinline__ void norm_heads_bwd(const NormRows& a, const E* in, c
       }
       ss = row_sum<LR>(ss);
       dot = row_sum<LR>(dot);
-      const float rs = rsqrtf(__fmaf_rn(ss, a.inv_K, a.eps));
+      const bool live = on && h0 + u * a.gpt < H;
+      // where there is no head nothing may reach the weight sums (eps may be 0)
+      const float rs = live ? rsqrtf(__fmaf_rn(ss, a.inv_K, a.eps)) : 0.f;
       const float m = __fmul_rn(__fmul_rn(rs, rs), __fmul_rn(dot, a.inv_K));
 #pragma unroll
       for (int i = 0; i < kNormV; ++i) {
-        gw[i] = __fmaf_rn(g[i], __fmul_rn(x[i], rs), gw[i]);  // x = 0 where there is no head
+        gw[i] = __fmaf_rn(g[i], __fmul_rn(x[i], rs), gw[i]);
         g[i] = __fmul_rn(rs, __fmaf_rn(-x[i], m, __fmul_rn(g[i], w[i])));
       }
-      if (on && h0 + u * a.gpt < H) {
+      if (live) {
         pg[u].set(g);
         pg[u].store(gin + base + (int64_t)(h0 + u * a.gpt) * a.K);
       }

@@ -181,3 +181,19 @@ def test_entries_from_R_on_are_left_as_they_are(S, il):
     fine = torch.ones(K, dtype=torch.bool, device="cuda")
     fine[R + 3] = False
     assert torch.equal(torch.isfinite(gw), fine)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hk,K,R", [(1, 3, 3, 1, 64, 64), (2, 45, 5, 2, 80, 16), (1, 701, 33, 6, 16, 0)])
+def test_no_eps(S, O, dtype, B, T, Hq, Hk, K, R):
+    """eps = 0 with heads and tokens that leave some lanes without a row: their
+    reciprocal root of nothing stays out of the weight sums."""
+    i, rng = draw(dtype, T, q=(B, T, Hq * K), k=(B, T, Hk * K), gq=(B, T, Hq * K), gk=(B, T, Hk * K))
+    wq, wk = rng.uniform(0.5, 1.5, size=(2, K)).astype(np.float32)
+    f, pos = freqs(R) if R else None, np.broadcast_to(np.arange(T), (B, T))
+    back = S.wkv_norm_rotate_backward(dev(i["q"]), dev(i["k"]), dev(i["gq"]), dev(i["gk"]), dev(wq), dev(wk),
+                                      None if f is None else dev(f), head_size=K, eps=0.0)
+    for j, (n, w) in enumerate((("q", wq), ("k", wk))):
+        rg, rw = O.norm_rotate_backward(i[n + "32"], i["g" + n + "32"], w, f, pos, K, 0.0, False)
+        assert rel_err(host64(back[j]), rg) < TOL_G[dtype], "g" + n
+        assert rel_err(host64(back[2 + j]), rw) < TOL_SUM, "gw" + n
