@@ -15,6 +15,8 @@
 // rest lie in shared memory in each order.
 #pragma once
 
+#include <float.h>
+
 #include "ssm_device.cuh"
 
 namespace wkv {
@@ -235,11 +237,17 @@ __device__ __forceinline__ void st_states_wide(float* p, int64_t N, const States
     *reinterpret_cast<float4*>(b) = make_float4(s.n[0].y, s.n[1].y, s.n[2].y, s.n[3].y);
   }
 }
+// A log2 e, so that a decay is one exponential. Kept finite: d = 0, which
+// passes over the tokens behind the last, must give a decay of 1 for any rate.
+__device__ __forceinline__ float scan_rate(float A) {
+  const float r = __fmul_rn(A, kLog2e);
+  return r < -FLT_MAX ? -FLT_MAX : r;
+}
 template <int S>
-__device__ __forceinline__ States<S> scale_states(const States<S>& s, float f) {
+__device__ __forceinline__ States<S> scan_rates(const States<S>& A) {
   States<S> r;
 #pragma unroll
-  for (int j = 0; j < S; ++j) r.n[j] = mul2(s.n[j], splat2(f));
+  for (int j = 0; j < S; ++j) r.n[j] = make_float2(scan_rate(A.n[j].x), scan_rate(A.n[j].y));
   return r;
 }
 

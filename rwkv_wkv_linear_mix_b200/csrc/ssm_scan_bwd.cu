@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
   const bool ch_on = 2 * pair < channels, on = ch_on && S * g < p.N;
   const int64_t nck = (T + kScanTile - 1) / kScanTile;
   const int64_t state_at = (w.b * p.C + c) * p.N + S * g;
-  const States<S> A2 = scale_states<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order), kLog2e);
+  const States<S> A2 = scan_rates<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order));
   States<S> gA = ld_states<S>(nullptr, 0, false, order);
   States<S> q = ld_states<S>(p.g_final + state_at, p.N, on && p.g_final, order);  // a_{t+1} Q_{t+1}
   const float D = p.D && ch_on ? p.D[c + order.swap] : 0.f;
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_bwd_carry_k
   const int pair = tid / LPC, g = tid % LPC;
   const int64_t c = w.c0 + 2 * pair;
   const bool on = 2 * pair < channels && S * g < p.N;
-  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, on), kLog2e);
+  const States<S> A2 = scan_rates<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, on));
   States<S> q = ld_states_wide<S>(nullptr, 0, false);
   float2 sum_d = splat2(0.f);
   load(nt - 1);

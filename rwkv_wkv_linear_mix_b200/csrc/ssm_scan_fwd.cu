@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
   const LaneOrder order{swap, 0};
   const int64_t c = w.c0 + 2 * pair;
   const bool ch_on = 2 * pair < channels, on = ch_on && S * g < p.N;  // channel counts are even
-  const States<S> A2 = scale_states<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order), kLog2e);
+  const States<S> A2 = scan_rates<S>(ld_states<S>(p.A + c * p.N + S * g, p.N, on, order));
   const float D = MODE != kScanCarry && p.D && ch_on ? p.D[c + swap] : 0.f;
   const int64_t state_at = (w.b * p.C + c) * p.N + S * g;
   States<S> h = ld_states<S>(p.init_state + state_at, p.N, MODE != kScanCarry && on && p.init_state, order);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanP
       pc[u].load(static_cast<const E*>(p.Cm) + (s * p.G + grp) * p.N + S * g);
     }
   }
-  const States<S> A2 = scale_states<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, state_on), kLog2e);
+  const States<S> A2 = scan_rates<S>(ld_states_wide<S>(p.A + c * p.N + S * g, p.N, state_on));
   const float2 bias = p.dt_bias ? ld_pair(p.dt_bias + c) : splat2(0.f);
   const float2 D = p.D ? ld_pair(p.D + c) : splat2(0.f);
 #pragma unroll

@@ -299,3 +299,25 @@ def test_backward_on_a_side_stream_and_in_a_graph(S):
     torch.cuda.synchronize()
     want = [t for t in (*S.wkv_scan_forward(*pos, **kw), *S.wkv_scan_backward(*pos, gy, **kw)) if t is not None]
     assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+@pytest.mark.parametrize("T", [1, 17, 300])
+def test_rate_of_minus_infinity(S, T):
+    """A state with A = -inf forgets at every token, as with any rate whose
+    decay is 0, whether or not the last tile is whole."""
+    C, N = 64, 16
+    i = draw("f32", (2, T), C, N, 1, seed=T)
+    pos, kw, _ = operands(i)
+    runs = []
+    for rate in (float("-inf"), -1e30):
+        pos[2] = dev(i["A"])
+        pos[2][::3, 1::4] = rate
+        y, fin, ck = S.wkv_scan_forward(*pos, init_state=dev(i["h0"]), want_ckpt=True, **kw)
+        grads = S.wkv_scan_backward(*pos, dev(i["gy"]), init_state=dev(i["h0"]), g_final=dev(i["gf"]), ckpt=ck,
+                                    want_g_init=True, **kw)
+        state = dev(i["h0"])
+        one = S.wkv_scan_decode_step(*(a[:, 0].contiguous() for a in pos[:2]), pos[2],
+                                     *(a[:, 0].contiguous() for a in pos[3:]), state, **{**kw, "z": kw["z"][:, 0].contiguous()})
+        runs.append([y, fin, *grads, one, state])
+    for a, b in zip(*runs):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
