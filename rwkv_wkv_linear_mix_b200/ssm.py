@@ -67,7 +67,7 @@ def _call(name: str, dev: torch.device, *args):
 
 def _has(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
     """The tensor's address, once it is known to be what the call reads or writes."""
-    if not (t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
         _want(t, name, dtype=dtype, shape=shape, device=dev)
     return t.data_ptr()
 
@@ -95,6 +95,17 @@ def _like(t: Optional[torch.Tensor], given: Optional[torch.Tensor], name: str, d
         given = torch.empty_like(t)
         return given, given.data_ptr()
     return given, _has(given, name, dtype, shape, dev)
+
+
+def _float32(want: bool, given: Optional[torch.Tensor], like: torch.Tensor, name: str, shape, dev):
+    """(tensor, address) of a float32 output: the one given, checked, or where
+    wanted a new one on the device of the float32 tensor `like`; else (None, None)."""
+    if given is not None:
+        return given, _has(given, name, torch.float32, shape, dev)
+    if not want:
+        return None, None
+    given = like.new_empty(shape)
+    return given, given.data_ptr()
 
 
 def _space(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
@@ -169,8 +180,8 @@ def wkv_conv_chunk_step(x, weight, cu_tokens: torch.Tensor, state: torch.Tensor,
     W, S, f32 = _taps(weight, C), state.shape[0], torch.float32
     y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
     _call("wkv_conv_chunk_step", dev, S, C, code, W, int(silu), x.data_ptr(),
-          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp, n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
-          _has(state, "state", x.dtype, (S, W - 1, C), dev))
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp, n,
+          _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev), _has(state, "state", x.dtype, (S, W - 1, C), dev))
     return y
 
 
@@ -181,7 +192,8 @@ def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: boo
     W, f32 = _taps(weight, C), torch.float32
     y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
     _call("wkv_conv_decode_step", dev, S, C, code, W, int(silu), x.data_ptr(),
-          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp, _has(state, "state", x.dtype, (S, W - 1, C), dev))
+          _has(weight, "weight", f32, (W, C), dev), _may(bias, "bias", f32, (C,), dev), yp,
+          _has(state, "state", x.dtype, (S, W - 1, C), dev))
     return y
 
 
@@ -276,16 +288,19 @@ def scan_ckpt_shape(B: int, T: int, C: int, N: int):
 def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dims):
     """(device, dtype code, sizes, addresses of the operands) of a scan over x of `dims` dimensions."""
     dev, code = _first(x, "x", dims)
-    lead, C = tuple(x.shape[:-1]), x.shape[-1]
-    if A.dim() != 2 or A.shape[0] != C:
-        raise ValueError(f"A must be [C, N] with C = {C}, got {tuple(A.shape)}")
-    N, f32, e = A.shape[1], torch.float32, x.dtype
-    if Bm.dim() != dims or N == 0 or Bm.shape[-1] % N:
-        raise ValueError(f"Bm must be [..., G * N] with N = {N}, got {tuple(Bm.shape)}")
-    G, bc = Bm.shape[-1] // N, (*lead, Bm.shape[-1])
-    return dev, code, lead, C, N, G, (
-        x.data_ptr(), _has(dt, "dt", e, x.shape, dev), _has(A, "A", f32, (C, N), dev), _has(Bm, "Bm", e, bc, dev),
-        _has(Cm, "Cm", e, bc, dev), _may(D, "D", f32, (C,), dev), _may(z, "z", e, x.shape, dev),
+    shape, f32, e = x.shape, torch.float32, x.dtype
+    *lead, C = shape
+    rates, bc = A.shape, Bm.shape
+    if len(rates) != 2 or rates[0] != C:
+        raise ValueError(f"A must be [C, N] with C = {C}, got {tuple(rates)}")
+    N = rates[1]
+    if len(bc) != dims or N == 0 or bc[-1] % N:
+        raise ValueError(f"Bm must be [..., G * N] with N = {N}, got {tuple(bc)}")
+    GN = bc[-1]
+    bc = (*lead, GN)
+    return dev, code, lead, C, N, GN // N, (
+        x.data_ptr(), _has(dt, "dt", e, shape, dev), _has(A, "A", f32, (C, N), dev), _has(Bm, "Bm", e, bc, dev),
+        _has(Cm, "Cm", e, bc, dev), _may(D, "D", f32, (C,), dev), _may(z, "z", e, shape, dev),
         _may(dt_bias, "dt_bias", f32, (C,), dev))
 
 
@@ -297,17 +312,12 @@ def wkv_scan_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state=
     Returns (y, final_state or None), or (y, final_state or None, ckpt) when
     ``want_ckpt`` (or a ckpt buffer is passed)."""
     dev, code, (B, T), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
-    f32 = torch.float32
     y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
-    if final_state is None and want_final_state:
-        final_state = torch.empty((B, C, N), dtype=f32, device=dev)
-    if ckpt is None and want_ckpt:
-        ckpt = torch.empty(scan_ckpt_shape(B, T, C, N), dtype=f32, device=dev)
+    final_state, fp = _float32(want_final_state, final_state, A, "final_state", (B, C, N), dev)
+    ckpt, cp = _float32(want_ckpt, ckpt, A, "ckpt", scan_ckpt_shape(B, T, C, N), dev)
     ptr, nbytes, workspace = _space(workspace, _fn["wkv_scan_forward_workspace_bytes"](B, T, C, N, G), dev)
     _call("wkv_scan_forward", dev, B, T, C, N, G, code, *ptrs, int(dt_softplus),
-          _may(init_state, "init_state", f32, (B, C, N), dev), yp,
-          _may(final_state, "final_state", f32, (B, C, N), dev),
-          _may(ckpt, "ckpt", f32, scan_ckpt_shape(B, T, C, N), dev), ptr, nbytes)
+          _may(init_state, "init_state", torch.float32, (B, C, N), dev), yp, fp, cp, ptr, nbytes)
     return (y, final_state) if ckpt is None else (y, final_state, ckpt)
 
 
@@ -331,7 +341,7 @@ def wkv_scan_backward(x, dt, A, Bm, Cm, gy, D=None, z=None, dt_bias=None, init_s
     gA, gB, gC = torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(Cm)
     gD = None if D is None else torch.empty_like(D)
     gbias = None if dt_bias is None else torch.empty_like(dt_bias)
-    g_init = torch.empty((B, C, N), dtype=f32, device=dev) if want_g_init else None
+    g_init = A.new_empty((B, C, N)) if want_g_init else None
     ptr, nbytes, workspace = _space(
         workspace, _fn["wkv_scan_backward_workspace_bytes"](B, T, C, N, G, int(ckpt is not None)), dev)
     _call("wkv_scan_backward", dev, B, T, C, N, G, code, *ptrs, int(dt_softplus),
@@ -350,8 +360,8 @@ def wkv_scan_chunk_step(x, dt, A, Bm, Cm, cu_tokens: torch.Tensor, state: torch.
     dev, code, (n,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
     S = state.shape[0]
     y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
-    _call("wkv_scan_chunk_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp, n, _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev),
-          _has(state, "state", torch.float32, (S, C, N), dev))
+    _call("wkv_scan_chunk_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp, n,
+          _has(cu_tokens, "cu_tokens", torch.int32, (S + 1,), dev), _has(state, "state", torch.float32, (S, C, N), dev))
     return y
 
 
@@ -361,5 +371,6 @@ def wkv_scan_decode_step(x, dt, A, Bm, Cm, state: torch.Tensor, D=None, z=None, 
     wkv_scan_chunk_step."""
     dev, code, (S,), C, N, G, ptrs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
     y, yp = _like(x, y, "y", x.dtype, x.shape, dev)
-    _call("wkv_scan_decode_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp, _has(state, "state", torch.float32, (S, C, N), dev))
+    _call("wkv_scan_decode_step", dev, S, C, N, G, code, *ptrs, int(dt_softplus), yp,
+          _has(state, "state", torch.float32, (S, C, N), dev))
     return y
