@@ -308,7 +308,7 @@ WKV_EXPORT size_t wkv_scan_ckpt_floats(int64_t B, int64_t T, int64_t C, int64_t 
 
 WKV_EXPORT size_t wkv_scan_forward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
   if (!scan_sizes_ok(B, T, C, N, G)) return 0;
-  return (size_t)scan_carry_floats(B, C, N, scan_fwd_cut(B, T, C, N, G).nseg) * sizeof(float);
+  return (size_t)scan_carry_floats(B, C, N, scan_fwd_cut(B, T, C, N, G)) * sizeof(float);
 }
 
 // The backward's workspace: partial sums, the pieces of the reverse walk,
@@ -326,12 +326,12 @@ static ScanBwdSpace scan_bwd_space(int64_t B, int64_t T, int64_t C, int64_t N, i
     return here;
   };
   w.bc = take(2 * (size_t)scan_group_blocks(C, N, G) * B * T * G * N);
-  w.a = take((size_t)B * cut.nseg * C * N);
-  w.d = take(2 * (size_t)B * cut.nseg * C);
-  w.carry = take((size_t)scan_carry_floats(B, C, N, cut.nseg));
+  w.a = take((size_t)cut.rows(B) * C * N);
+  w.d = take(2 * (size_t)cut.rows(B) * C);
+  w.carry = take((size_t)scan_carry_floats(B, C, N, cut));
   if (!has_ckpt) {
     w.ckpt = take(wkv_scan_ckpt_floats(B, T, C, N));
-    w.fwd = take((size_t)scan_carry_floats(B, C, N, scan_fwd_cut(B, T, C, N, G).nseg));
+    w.fwd = take((size_t)scan_carry_floats(B, C, N, scan_fwd_cut(B, T, C, N, G)));
   }
   w.total = at;
   return w;

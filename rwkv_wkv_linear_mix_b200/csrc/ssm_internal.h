@@ -98,7 +98,7 @@ struct ScanArgs {
   void* y;
   float* final_state;
   float* ckpt;
-  float* carry;  // pieces of a cut sequence: [B][nseg][C][N] states, then [B][nseg][C] sums of d
+  float* carry;  // of the cut sequences: [sequence][nseg][C][N] states, then [sequence][nseg][C] sums of d
   int64_t n_tokens;
   const int32_t* cu;  // slots, else null
 };
@@ -116,8 +116,8 @@ struct ScanBwdArgs {
   float* gdt_bias;
   float* g_init;
   float* part_bc;  // [2][blocks per group][B*T][G*N]
-  float* part_a;   // [B*nseg][C][N]
-  float* part_d;   // [2][B*nseg][C]: gD, gdt_bias
+  float* part_a;   // [pieces of all sequences][C][N]
+  float* part_d;   // [2][pieces of all sequences][C]: gD, gdt_bias
 };
 // State sizes the kernels are built for.
 inline int scan_padded_states(int64_t N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
@@ -127,15 +127,18 @@ constexpr int scan_cta_channels(int states) { return states <= 8 ? 64 : states <
 inline int64_t scan_group_blocks(int64_t C, int64_t N, int64_t G) {
   return ceil_div(C / std::max<int64_t>(G, 1), scan_cta_channels(scan_padded_states(N)));
 }
-// Pieces along T (1: uncut) of the forward and of the backward; each but the
-// last has seg_tiles * WKV_SCAN_CKPT_LEN tokens.
+// How a launch is cut along T: the first `whole` sequences are not, the others
+// are, into nseg pieces, each but the last of seg_tiles * WKV_SCAN_CKPT_LEN
+// tokens. nseg is 1 where none is cut.
 struct ScanCut {
+  int64_t whole;
   int nseg, seg_tiles;
+  int64_t rows(int64_t B) const { return whole + (B - whole) * nseg; }  // pieces of all sequences
 };
 ScanCut scan_fwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G);
 ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G);
-inline int64_t scan_carry_floats(int64_t B, int64_t C, int64_t N, int nseg) {
-  return nseg > 1 ? B * nseg * C * (N + 1) : 0;
+inline int64_t scan_carry_floats(int64_t B, int64_t C, int64_t N, const ScanCut& cut) {
+  return (B - cut.whole) * cut.nseg * C * (N + 1);
 }
 wkv_status launch_scan_forward(const ScanArgs& a, cudaStream_t stream, const char** why);
 wkv_status launch_scan_chunk_step(const ScanArgs& a, cudaStream_t stream, unsigned* err, const char** why);

@@ -41,7 +41,7 @@ struct ScanGeom {
 
 struct ScanParams {
   int64_t B, T, C, N, G, Cg;  // Cg = C / G
-  int nbg, nseg;              // CTAs per group; pieces along T
+  int nbg, nseg;              // CTAs per group; pieces of a cut sequence
   int64_t seg_tokens;
   int softplus;
   const void *x, *dt, *Bm, *Cm, *z;
@@ -57,21 +57,33 @@ struct ScanParams {
   const float* g_final;
   void *gx, *gdt, *gz;
   float *g_init, *part_bc, *part_a, *part_d;
+  // sequences that are not cut; pieces of all (here and not among the sizes,
+  // where the forward takes 350 us for 345: its parameters lie worse)
+  int64_t whole, rows;
 };
 
-// Where a CTA works: sequence b, piece seg, group g, channels c0 .. cend-1
-// (at most CB of them), block blk of the group.
+// Where a CTA works: sequence b, piece seg up to its last, of all pieces the
+// row-th, group g, channels c0 .. cend-1 (at most CB of them), block blk of
+// the group. The pieces of cut sequences come after the whole sequences; MIXED:
+// a launch may have both (the forward cuts all or none).
 struct ScanPlace {
-  int64_t b, c0, cend;
-  int g, blk, seg;
+  int64_t b, c0, cend, row;
+  int g, blk, seg, last;
 };
-template <int CB>
+template <int CB, bool MIXED>
 __device__ __forceinline__ ScanPlace scan_place(const ScanParams& p) {
   ScanPlace w;
   const unsigned ncb = (unsigned)(p.G * p.nbg);
-  const unsigned cb = blockIdx.x % ncb, rest = blockIdx.x / ncb;
-  w.seg = (int)(rest % (unsigned)p.nseg);
-  w.b = rest / (unsigned)p.nseg;
+  const unsigned cb = blockIdx.x % ncb, row = blockIdx.x / ncb, whole = MIXED ? (unsigned)p.whole : 0;
+  w.row = row;
+  if (MIXED && row < whole) {
+    w.seg = w.last = 0;
+    w.b = row;
+  } else {
+    w.seg = (int)((row - whole) % (unsigned)p.nseg);
+    w.last = p.nseg - 1;
+    w.b = whole + (row - whole) / (unsigned)p.nseg;
+  }
   w.g = (int)(cb / (unsigned)p.nbg);
   w.blk = (int)(cb % (unsigned)p.nbg);
   w.c0 = w.g * p.Cg + (int64_t)w.blk * CB;
@@ -315,12 +327,31 @@ __device__ __forceinline__ void pair_sums(float (&v)[4], float (&out)[kPairSums<
   for (int t = 0; t < kPairSums<LPC>; ++t) out[t] = v[t];
 }
 
+// Host: the sequences from `whole` on in at most nseg pieces, each of at least
+// 4 tiles.
+inline ScanCut scan_cut(int64_t B, int64_t whole, int64_t nseg, int64_t T) {
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(T, kScanTile));
+  const int64_t per = ceil_div(tiles, std::max<int64_t>(1, std::min(nseg, tiles / 4)));
+  const int64_t n = ceil_div(tiles, per);
+  return ScanCut{n > 1 ? whole : B, (int)n, (int)per};
+}
+// A launch with `ctas` CTAs per sequence. With fewer than two per SM in all,
+// every sequence is cut for about eight per SM, which is what an SM holds
+// (four: 205 against 176 us at B=1 T=8191 C=1536); else none is, since the
+// carry pass costs most of a second walk (B=2 C=4096, 256 CTAs, cut and uncut:
+// 217 and 209 us forward, 502 and 522 backward; B=4: 387 and 303, 921 and 852).
+inline ScanCut scan_cut_few(int64_t B, int64_t ctas, int64_t T) {
+  const int64_t all = std::max<int64_t>(1, B * ctas);
+  return all < 148 * 2 ? scan_cut(B, 0, ceil_div(148 * 8, all), T) : scan_cut(B, B, 1, T);
+}
+
 // Host: the parameters a launch has in common.
 inline ScanParams scan_params(const ScanArgs& a, const ScanCut& cut) {
   ScanParams p{};
   p.B = a.B, p.T = a.T, p.C = a.C, p.N = a.N, p.G = a.G, p.Cg = a.C / a.G;
   p.nbg = (int)scan_group_blocks(a.C, a.N, a.G);
   p.nseg = cut.nseg;
+  p.whole = cut.whole, p.rows = cut.rows(a.B);
   p.seg_tokens = (int64_t)cut.seg_tiles * kScanTile;
   p.softplus = a.softplus;
   p.x = a.x, p.dt = a.dt, p.Bm = a.Bm, p.Cm = a.Cm, p.z = a.z;

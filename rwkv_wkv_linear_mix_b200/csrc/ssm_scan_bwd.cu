@@ -99,19 +99,22 @@ struct ChannelSums {
   __device__ static __forceinline__ int token(int v, int lane) { return TOK ? (lane / (LPC * PS)) & 1 : v / GS; }
 };
 
+// CTAs of the backward that an SM holds, by states per thread.
+constexpr int scan_bwd_resident(int S) { return S == 2 ? 4 : 2; }
+
 template <class E, int LPC, int S, bool Z>
-__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) scan_bwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_resident(S)) scan_bwd_kernel(const ScanParams p) {
   using Geo = ScanGeom<E, LPC, S>;
   using Shared = ScanBwdShared<E, Geo>;
   constexpr int NP = Geo::NP, WARPS = Shared::WARPS, SUB = kBwdSub;
   using Sums = ChannelSums<LPC, S>;
   extern __shared__ float4 smem4[];
   Shared& sm = *reinterpret_cast<Shared*>(smem4);
-  const ScanPlace w = scan_place<Geo::CB>(p);
+  const ScanPlace w = scan_place<Geo::CB, true>(p);
   const int tid = threadIdx.x;
   const int64_t T = p.T, first = w.b * T;
   const int64_t tbeg = w.seg * p.seg_tokens;
-  const int64_t tend = w.seg == p.nseg - 1 ? T : tbeg + p.seg_tokens;
+  const int64_t tend = w.seg == w.last ? T : tbeg + p.seg_tokens;
   const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
   const int64_t GN = p.G * p.N, gN = w.g * p.N;
   const int channels = (int)(w.cend - w.c0);
@@ -172,11 +175,11 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
   States<S> q = ld_states<S>(p.g_final + state_at, p.N, on && p.g_final, order);  // a_{t+1} Q_{t+1}
   const float D = p.D && ch_on ? p.D[c + order.swap] : 0.f;
   {
-    const float* sums = p.carry + p.B * p.nseg * p.C * p.N;
+    const float* sums = p.carry + (p.B - p.whole) * p.nseg * p.C * p.N;
     if (on) {
 #pragma unroll 8
-      for (int j = p.nseg - 1; j > w.seg; --j) {
-        const int64_t row = (w.b * p.nseg + j) * p.C + c;
+      for (int j = w.last; j > w.seg; --j) {
+        const int64_t row = ((w.b - p.whole) * p.nseg + j) * p.C + c;
         const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
         scan_fold(q, scan_decay(make_float2(sums[row + order.swap], sums[row + 1 - order.swap]), A2), s);
       }
@@ -332,8 +335,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
   }
   put_sums(0);
 
-  const int64_t prow = w.b * p.nseg + w.seg;
-  if (on) st_states<S>(p.part_a + (prow * p.C + c) * p.N + S * g, p.N, gA, order);
+  if (on) st_states<S>(p.part_a + (w.row * p.C + c) * p.N + S * g, p.N, gA, order);
   if (on && p.g_init && w.seg == 0) st_states<S>(p.g_init + state_at, p.N, q, order);
   // over the lanes of the channel, each of which finished other tokens
 #pragma unroll
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 4 : 2) 
     gdb = __fadd_rn(gdb, __shfl_xor_sync(0xffffffffu, gdb, m));
   }
   if (ch_on && g < 2) {
-    p.part_d[prow * p.C + c + g] = gD;
-    p.part_d[(p.B * p.nseg + prow) * p.C + c + g] = gdb;
+    p.part_d[w.row * p.C + c + g] = gD;
+    p.part_d[(p.rows + w.row) * p.C + c + g] = gdb;
   }
 }
 
@@ -359,12 +361,12 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_bwd_carry_k
   using Geo = ScanGeom<E, LPC, S>;
   extern __shared__ float4 smem4[];
   auto& sm = *reinterpret_cast<ScanBwdCarryShared<E, Geo>*>(smem4);
-  const ScanPlace w = scan_place<Geo::CB>(p);
+  const ScanPlace w = scan_place<Geo::CB, true>(p);
   if (w.seg == 0) return;  // nothing lies below the first piece
   const int tid = threadIdx.x;
   const int64_t first = w.b * p.T;
   const int64_t tbeg = w.seg * p.seg_tokens;
-  const int64_t tend = w.seg == p.nseg - 1 ? p.T : tbeg + p.seg_tokens;
+  const int64_t tend = w.seg == w.last ? p.T : tbeg + p.seg_tokens;
   const int nt = (int)((tend - tbeg + kScanTile - 1) / kScanTile);
   const int64_t GN = p.G * p.N;
   const int channels = (int)(w.cend - w.c0);
@@ -429,9 +431,9 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS) scan_bwd_carry_k
     copy_async_wait();
     __syncthreads();
   }
-  const int64_t row = (w.b * p.nseg + w.seg) * p.C + c;
+  const int64_t row = ((w.b - p.whole) * p.nseg + w.seg) * p.C + c;
   if (on) st_states_wide<S>(p.carry + row * p.N + S * g, p.N, q, 0);
-  if (on && g == 0) st_pair(p.carry + p.B * p.nseg * p.C * p.N + row, sum_d);
+  if (on && g == 0) st_pair(p.carry + (p.B - p.whole) * p.nseg * p.C * p.N + row, sum_d);
 }
 
 // gB and gC: the sum of the CTAs' partial rows, in order, in the storage type.
@@ -466,7 +468,7 @@ wkv_status run_shared(K kernel, const ScanParams& p, int threads, size_t smem, c
     *why = what;
     return WKV_ERR_CUDA;
   }
-  kernel<<<(unsigned)(p.B * p.nseg * p.G * p.nbg), threads, smem, st>>>(p);
+  kernel<<<(unsigned)(p.rows * p.G * p.nbg), threads, smem, st>>>(p);
   return launched(what, why);
 }
 
@@ -494,7 +496,7 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
                                                                             static_cast<E*>(b.gC));
   if (wkv_status s = launched("scan gB, gC sum kernel launch failed", why)) return s;
   SumRows sums{};
-  sums.rows = a.B * cut.nseg;
+  sums.rows = cut.rows(a.B);
   sums.add(b.part_a, a.C * a.N, b.gA);
   sums.add(b.part_d, a.C, b.gD);
   sums.add(b.part_d + sums.rows * a.C, a.C, b.gdt_bias);
@@ -502,6 +504,22 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
 }
 
 }  // namespace
+
+// More CTAs than fit at once leave a last wave that idles most SMs. The
+// sequences past the last even share of the SMs are cut then, into small
+// pieces that fill the gaps, if the share of the time that idles is above
+// what their carry pass takes, about a quarter of their walk (T=2048 C=2560,
+// 640 CTAs: 1044 -> 900 us at B=8; 960 CTAs: 706 -> 681; where all fit at
+// once it does not pay: 384 CTAs, 652 -> 737).
+ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
+  const int64_t ctas = G * scan_group_blocks(C, N, G), all = B * ctas;
+  if (all > 148 * scan_bwd_resident(scan_padded_states(N) <= 16 ? 2 : 4)) {
+    const int64_t whole = all / 148 * 148 / ctas;
+    const double idle = 1. - (double)all / (double)(148 * ceil_div(all, 148));
+    if (idle > 0.25 * (double)(B - whole) / (double)B) return scan_cut(B, whole, 8, T);
+  }
+  return scan_cut_few(B, ctas, T);
+}
 
 wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const char** why) {
   const bool bf = a.f.dtype == WKV_BF16;

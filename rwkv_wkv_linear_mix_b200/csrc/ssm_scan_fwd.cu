@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
   using Geo = ScanGeom<E, LPC, S>;
   extern __shared__ float4 smem4[];
   auto& sm = *reinterpret_cast<ScanFwdShared<E, Geo>*>(smem4);
-  const ScanPlace w = scan_place<Geo::CB>(p);
+  const ScanPlace w = scan_place<Geo::CB, false>(p);
   const int tid = threadIdx.x;
   if (MODE == kScanCarry && w.seg == p.nseg - 1) return;  // nothing follows the last piece
   int64_t first = w.b * p.T, T = p.T;
@@ -263,7 +263,7 @@ wkv_status run_walk(const ScanParams& p, cudaStream_t st, const char** why) {
     *why = "scan kernel: shared memory request failed";
     return WKV_ERR_CUDA;
   }
-  const int64_t grid = p.B * p.nseg * p.G * p.nbg;
+  const int64_t grid = p.rows * p.G * p.nbg;
   scan_fwd_kernel<E, LPC, S, MODE><<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
   return launched("scan kernel launch failed", why);
 }
@@ -291,13 +291,13 @@ wkv_status run_forward(const ScanArgs& a, cudaStream_t st, const char** why) {
 }
 template <class E, int LPC, int S>
 wkv_status run_slots(const ScanArgs& a, cudaStream_t st, unsigned* err, const char** why) {
-  ScanParams p = scan_params(a, ScanCut{1, 0});
+  ScanParams p = scan_params(a, ScanCut{a.B, 1, 0});
   p.err = err;
   return run_walk<E, LPC, S, kScanSlots>(p, st, why);
 }
 template <class E, int LPC, int S>
 wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
-  const ScanParams p = scan_params(a, ScanCut{1, 0});
+  const ScanParams p = scan_params(a, ScanCut{a.B, 1, 0});
   constexpr int DL = LPC * S / 4;  // a stream of states: 16 bytes per lane and channel
   const int64_t threads = ceil_div(a.B, kDecodeSlots) * (a.C / 2) * DL;
   scan_decode_kernel<E, DL, 4><<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
@@ -317,26 +317,10 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
     default: return bf ? CALL(__nv_bfloat16, 16, 4) : CALL(float, 16, 4);         \
   }
 
-// Pieces along T: none where the channels alone give two CTAs per SM, since
-// the carry pass costs most of a second walk (B=2 C=4096, 256 CTAs, cut and
-// uncut: 217 and 209 us forward, 502 and 522 backward; B=4: 387 and 303, 921
-// and 852); else about eight CTAs per SM, which is what an SM holds (four: 205
-// against 176 us at B=1 T=8191 C=1536), in pieces of at least 4 tiles.
-ScanCut cut_for(int64_t ctas, int64_t T) {
-  const int64_t tiles = std::max<int64_t>(1, ceil_div(T, kScanTile));
-  int64_t nseg = 1;
-  if (ctas < 148 * 2) nseg = std::min(ceil_div(148 * 8, std::max<int64_t>(1, ctas)), std::max<int64_t>(1, tiles / 4));
-  const int64_t per = ceil_div(tiles, nseg);
-  return ScanCut{(int)ceil_div(tiles, per), (int)per};
-}
-
 }  // namespace
 
 ScanCut scan_fwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
-  return cut_for(B * G * scan_group_blocks(C, N, G), T);
-}
-ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
-  return cut_for(B * G * scan_group_blocks(C, N, G), T);
+  return scan_cut_few(B, G * scan_group_blocks(C, N, G), T);
 }
 
 wkv_status launch_scan_forward(const ScanArgs& a, cudaStream_t stream, const char** why) {

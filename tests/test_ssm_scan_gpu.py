@@ -321,3 +321,31 @@ def test_rate_of_minus_infinity(S, T):
         runs.append([y, fin, *grads, one, state])
     for a, b in zip(*runs):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,B,T,C,N,G", [("bf16", 20, 121, 1024, 16, 1), ("f32", 20, 160, 1024, 12, 1),
+                                             ("f32", 5, 150, 1024, 64, 1), ("bf16", 10, 200, 1024, 32, 2),
+                                             ("bf16", 10, 130, 4096, 8, 1)])
+def test_backward_of_more_than_one_wave(S, O, dtype, B, T, C, N, G):
+    """CTAs for a little more than one wave: the last sequences are cut along T
+    and the others are not. The last three against the oracle; the parameter
+    gradients against its sums and those of a call on the others."""
+    i = draw(dtype, (B, T), C, N, G, seed=N)
+    pos, kw, ref = operands(i)
+    h0, gf, k = dev(i["h0"]), dev(i["gf"]), B - 3
+    _, _, ckpt = S.wkv_scan_forward(*pos, **kw, init_state=h0, want_ckpt=True)
+    got = dict(zip(NAMES, S.wkv_scan_backward(*pos, dev(i["gy"]), **kw, init_state=h0, g_final=gf, ckpt=ckpt, want_g_init=True)))
+    again = S.wkv_scan_backward(*pos, dev(i["gy"]), **kw, init_state=h0, g_final=gf, want_g_init=True)
+    assert all(torch.equal(a, b) for a, b in zip(got.values(), again))
+    head = [a if a.dim() == 2 else a[:k] for a in pos]
+    rest = dict(zip(NAMES, S.wkv_scan_backward(*head, dev(i["gy"])[:k], **{**kw, "z": kw["z"][:k]}, init_state=h0[:k],
+                                               g_final=gf[:k], want_g_init=True)))
+    ref = {n: a[k:] if n in ("x", "dt", "Bm", "Cm", "z") else a for n, a in ref.items()}
+    want = O.scan_backward(gy=i["gy32"][k:], init_state=i["h0"][k:], g_final=i["gf"][k:], **ref)
+    for n in NAMES:
+        if n in ("gA", "gD", "gdt_bias"):
+            assert rel_err(host64(got[n]), want[n] + host64(rest[n])) < 2 * TOL32, n  # of both sides
+        else:
+            tol = TOL32 if got[n].dtype == torch.float32 else TOL["bf16"]
+            assert rel_err(host64(got[n][k:]), want[n]) < tol, n
+            assert rel_err(host64(got[n][:k]), host64(rest[n])) < 2 * tol, n
