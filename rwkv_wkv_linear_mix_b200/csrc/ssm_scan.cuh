@@ -3,9 +3,10 @@
 //
 // A thread carries S = 2 or 4 states of each of 2 adjacent channels; LPC lanes
 // side by side share the pair, so that S LPC >= N. The states above N are zero
-// and stay zero (their B is zero). A CTA covers CB channels of one group, so
-// that B and C are one row of numbers per token for all of them, and walks its
-// tokens in tiles of 16.
+// and stay zero: their B and C are zero, and their lanes take d x and gs for
+// zero (an infinite d x of the channel times B = 0 would be NaN). A CTA covers
+// CB channels of one group, so that B and C are one row of numbers per token
+// for all of them, and walks its tokens in tiles of 16.
 //
 // Packed pairs hold one state of both channels. Sums over lanes are taken in
 // halving steps, and a lane's order of channels and states is chosen so that
@@ -261,6 +262,15 @@ __device__ __forceinline__ States<S> scan_rates(const States<S>& A) {
 #pragma unroll
   for (int j = 0; j < S; ++j) r.n[j] = make_float2(scan_rate(A.n[j].x), scan_rate(A.n[j].y));
   return r;
+}
+
+// A pair's d x or gs for a lane of states; zero for one without. Kernels are
+// built apart for N that leaves no such lane (PAD false), since the selects
+// cost 2 to 5 % of N=12 (B=4 T=2048 C=2048 bf16: forward 198 -> 202 us,
+// backward 474 -> 496; N=24: 324 -> 326, 828 -> 813).
+template <bool PAD>
+__device__ __forceinline__ float2 scan_taken(float x, float y, bool states) {
+  return !PAD || states ? make_float2(x, y) : splat2(0.f);
 }
 
 // The step sizes d of a pair of channels from what is stored.

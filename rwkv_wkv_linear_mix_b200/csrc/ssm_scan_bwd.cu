@@ -102,7 +102,7 @@ struct ChannelSums {
 // CTAs of the backward that an SM holds, by states per thread.
 constexpr int scan_bwd_resident(int S) { return S == 2 ? 4 : 2; }
 
-template <class E, int LPC, int S, bool Z>
+template <class E, int LPC, int S, bool PAD, bool Z>
 __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_resident(S)) scan_bwd_kernel(const ScanParams p) {
   using Geo = ScanGeom<E, LPC, S>;
   using Shared = ScanBwdShared<E, Geo>;
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
 
   const int pair = tid / LPC, g = tid % LPC, warp = tid / 32, lane = tid % 32;
   const LaneOrder order{g & 1, Sums::perm(lane)};
+  const bool states = S * g < p.N;
   const int64_t c = w.c0 + 2 * pair;
   const bool ch_on = 2 * pair < channels, on = ch_on && S * g < p.N;
   const int64_t nck = (T + kScanTile - 1) / kScanTile;
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
 #pragma unroll
     for (int t = 0; t < kScanTile - SUB; ++t) {
       const float4 dd = sm.dd[t][order.swap][pair];
-      scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[t][order.perm][S * g]));
+      scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), scan_taken<PAD>(dd.z, dd.w, states),
+                  ld_row<S>(&sm.B[t][order.perm][S * g]));
       if ((t + 1) % SUB == 0 && t + 1 < kScanTile - SUB) st_h((t + 1) / SUB, h);
     }
 #pragma unroll 1
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
 #pragma unroll
         for (int j = 0; j < S; ++j) {
           ah[t].n[j] = mul2(a[t].n[j], h.n[j]);
-          h.n[j] = fma2(make_float2(dd.z, dd.w), splat2(Bv.n[j]), ah[t].n[j]);
+          h.n[j] = fma2(scan_taken<PAD>(dd.z, dd.w, states), splat2(Bv.n[j]), ah[t].n[j]);
         }
       }
       // down again, the states formed anew from the decayed ones (which is
@@ -276,9 +278,9 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
         for (int u = 1; u >= 0; --u) {
           const int tt = tb + t + u;
           const float4 dd = sm.dd[tt][order.swap][pair];
-          const float2 gs = sm.gs[tt][order.swap][pair];
+          const float2 gss = sm.gs[tt][order.swap][pair], gs = scan_taken<PAD>(gss.x, gss.y, states);
           const Row<S> Bv = ld_row<S>(&sm.B[tt][order.perm][S * g]), Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
-          const float2 d = make_float2(dd.x, dd.y), dx = make_float2(dd.z, dd.w);
+          const float2 d = make_float2(dd.x, dd.y), dx = scan_taken<PAD>(dd.z, dd.w, states);
           States<S> Q, W, ht;
 #pragma unroll
           for (int j = 0; j < S; ++j) {
@@ -486,11 +488,11 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
     if (wkv_status s = run_shared(scan_bwd_carry_kernel<E, LPC, S>, p, Geo::THREADS, sizeof(ScanBwdCarryShared<E, Geo>), st,
                                   "scan backward carry kernel launch failed", why))
       return s;
-  if (wkv_status s = a.z ? run_shared(scan_bwd_kernel<E, LPC, S, true>, p, Geo::THREADS, smem, st,
-                                      "scan backward kernel launch failed", why)
-                         : run_shared(scan_bwd_kernel<E, LPC, S, false>, p, Geo::THREADS, smem, st,
-                                      "scan backward kernel launch failed", why))
-    return s;
+  const bool pad = a.N < Geo::NP;
+  const auto kernel = a.z ? pad ? scan_bwd_kernel<E, LPC, S, true, true> : scan_bwd_kernel<E, LPC, S, false, true>
+                      : pad ? scan_bwd_kernel<E, LPC, S, true, false>
+                            : scan_bwd_kernel<E, LPC, S, false, false>;
+  if (wkv_status s = run_shared(kernel, p, Geo::THREADS, smem, st, "scan backward kernel launch failed", why)) return s;
   const int64_t n4 = a.B * a.T * a.G * a.N / 4;
   scan_sum_bc_kernel<E><<<dim3((unsigned)ceil_div(n4, 256), 2), 256, 0, st>>>(b.part_bc, p.nbg, n4, static_cast<E*>(b.gB),
                                                                             static_cast<E*>(b.gC));

@@ -42,7 +42,7 @@ struct ScanFwdShared {
 // Seven CTAs of 4 warps per SM with two states per lane (72 registers): left
 // alone the compiler takes up to 168 (prompt, B=8 C=4096: 536 us against 452;
 // 9 CTAs, 56 registers: 463).
-template <class E, int LPC, int S, int MODE>
+template <class E, int LPC, int S, bool PAD, int MODE>
 __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) scan_fwd_kernel(const ScanParams p) {
   using Geo = ScanGeom<E, LPC, S>;
   extern __shared__ float4 smem4[];
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
       for (int j = 0; j < 4; ++j) {
         const float4 dd = sm.dd[tg + j][swap][pair];
         const float2 d = make_float2(dd.x, dd.y);
-        scan_absorb(h, scan_decay(d, A2), make_float2(dd.z, dd.w), ld_row<S>(&sm.B[tg + j][S * g]));
+        scan_absorb(h, scan_decay(d, A2), scan_taken<PAD>(dd.z, dd.w, S * g < p.N), ld_row<S>(&sm.B[tg + j][S * g]));
         if constexpr (MODE != kScanCarry)
           dots[j] = scan_dot<S>(h, ld_row<S>(&sm.C[tg + j][S * g]));
         else
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
 // the loads of both are in flight together and A is read once.
 constexpr int kDecodeThreads = 128;
 constexpr int kDecodeSlots = 2;  // 1: 31, 2: 27, 4: 28 us for 256 slots, C=4096 N=16 bf16
-template <class E, int LPC, int S>
+template <class E, int LPC, int S, bool PAD>
 __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanParams p) {
   constexpr int U = kDecodeSlots;
   const int64_t i = (int64_t)blockIdx.x * kDecodeThreads + threadIdx.x;
@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanP
     pb[u].get(Bv.n);
     pc[u].get(Cv.n);
     const float2 d = scan_step_size2(dt[u], bias, p.softplus);
-    scan_absorb(h[u], scan_decay(d, A2), mul2(d, x[u]), Bv);
+    const float2 dx = mul2(d, x[u]);
+    scan_absorb(h[u], scan_decay(d, A2), scan_taken<PAD>(dx.x, dx.y, state_on), Bv);
     if (state_on && there) st_states_wide<S>(p.final_state + ((s0 + u) * p.C + c) * p.N + S * g, p.N, h[u], 0);
     const float2 dot = scan_dot<S>(h[u], Cv);
     float out[2] = {dot.x, dot.y};
@@ -257,14 +258,16 @@ wkv_status run_walk(const ScanParams& p, cudaStream_t st, const char** why) {
   using Geo = ScanGeom<E, LPC, S>;
   constexpr size_t smem = sizeof(ScanFwdShared<E, Geo>);
   static_assert(smem <= 227 * 1024, "the tiles fit an SM");
+  // the carry adds nothing up over lanes and keeps no state of a lane without any
+  constexpr bool CAN_PAD = MODE != kScanCarry;
+  const auto kernel = p.N < Geo::NP ? scan_fwd_kernel<E, LPC, S, CAN_PAD, MODE> : scan_fwd_kernel<E, LPC, S, false, MODE>;
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(scan_fwd_kernel<E, LPC, S, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     *why = "scan kernel: shared memory request failed";
     return WKV_ERR_CUDA;
   }
   const int64_t grid = p.rows * p.G * p.nbg;
-  scan_fwd_kernel<E, LPC, S, MODE><<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
+  kernel<<<(unsigned)grid, Geo::THREADS, smem, st>>>(p);
   return launched("scan kernel launch failed", why);
 }
 
@@ -300,7 +303,8 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
   const ScanParams p = scan_params(a, ScanCut{a.B, 1, 0});
   constexpr int DL = LPC * S / 4;  // a stream of states: 16 bytes per lane and channel
   const int64_t threads = ceil_div(a.B, kDecodeSlots) * (a.C / 2) * DL;
-  scan_decode_kernel<E, DL, 4><<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
+  const auto kernel = a.N < LPC * S ? scan_decode_kernel<E, DL, 4, true> : scan_decode_kernel<E, DL, 4, false>;
+  kernel<<<(unsigned)ceil_div(threads, kDecodeThreads), kDecodeThreads, 0, st>>>(p);
   return launched("scan decode kernel launch failed", why);
 }
 
