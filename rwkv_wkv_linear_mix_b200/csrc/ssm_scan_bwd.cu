@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
         const int tt = tb + pair_sum_first<LPC>(g) + v;
         const float4 fin = sm.fin[tt][order.swap * Shared::FIN1 + pair];
         const float d = fin.x, x = fin.y, gs = sm.gs[tt][order.swap][pair].x;
-        const float rgx = __fmaf_rn(out[v], d, __fmul_rn(gs, D));
+        const float rgx = __fmaf_rn(out[v], d, p.D ? __fmul_rn(gs, D) : 0.f);  // (no product without D: gs may be infinite)
         const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
         if (tt < left && ch_on && g < 8) {
           const int64_t to = at + tt * (int)p.C;
           static_cast<E*>(p.gx)[to] = Elem<E>::from_f32(rgx);
           static_cast<E*>(p.gdt)[to] = Elem<E>::from_f32(graw);
           if constexpr (Z)
-            static_cast<E*>(p.gz)[to] = Elem<E>::from_f32(__fmul_rn(fin.w, __fmaf_rn(D, x, sv[v])));
+            static_cast<E*>(p.gz)[to] = Elem<E>::from_f32(__fmul_rn(fin.w, p.D ? __fmaf_rn(D, x, sv[v]) : sv[v]));
           gD = __fmaf_rn(gs, x, gD);
           gdb = __fadd_rn(gdb, graw);
         }

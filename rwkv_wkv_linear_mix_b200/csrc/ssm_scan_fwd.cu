@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, S == 2 ? 7 : 4) 
 #pragma unroll
         for (int v = 0; v < kPairSums<LPC>; ++v) {
           const int t = tg + out0 + v;
-          float o = __fadd_rn(done[tg / 4][v], __fmul_rn(D, Elem<E>::to_f32(raw.act[kActX][t][2 * pair + swap])));
+          const float x = Elem<E>::to_f32(raw.act[kActX][t][2 * pair + swap]), s = done[tg / 4][v];
+          float o = p.D ? __fmaf_rn(D, x, s) : s;  // (0 times an infinite x would be NaN)
           if (p.z) {
             const float z = Elem<E>::to_f32(raw.act[kActZ][t][2 * pair + swap]);
             o = __fmul_rn(o, __fmul_rn(z, sigmoid_f(z)));
@@ -240,9 +241,9 @@ __global__ void __launch_bounds__(kDecodeThreads) scan_decode_kernel(const ScanP
       out[1] = __fadd_rn(out[1], __shfl_xor_sync(0xffffffffu, out[1], m));
     }
     if (there && g == 0) {
-      const float2 gate = p.z ? mul2(z[u], sigmoid2(z[u])) : splat2(1.f), e = mul2(D, x[u]);
-      st_pair(static_cast<E*>(p.y) + (s0 + u) * p.C + c,
-              make_float2(__fmul_rn(__fadd_rn(out[0], e.x), gate.x), __fmul_rn(__fadd_rn(out[1], e.y), gate.y)));
+      const float2 sums = make_float2(out[0], out[1]), skip = p.D ? fma2(D, x[u], sums) : sums;
+      const float2 gate = p.z ? mul2(z[u], sigmoid2(z[u])) : splat2(1.f);
+      st_pair(static_cast<E*>(p.y) + (s0 + u) * p.C + c, mul2(skip, gate));
     }
   }
 }

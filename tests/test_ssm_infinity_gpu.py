@@ -114,3 +114,33 @@ def test_slots_and_single_tokens(S, O, N):
         ry, rlast = O.scan_forward(**tok, init_state=i["h0"])
     same(y1, ry[:, 0], "single tokens")
     same(state1, rlast, "state")
+
+
+@pytest.mark.parametrize("gate", [True, False])
+def test_without_a_skip_term(S, O, gate):
+    """With no D there is no product of it: an infinite x gives an infinite y
+    and gz, an infinite gy an infinite gx."""
+    i = draw((2, 48), 24, 16, 1, 7, 2)
+    i["x"][0, 5, 3] = INF
+    i["gy"][1, 20, 8] = INF
+    pos, kw = put(i)
+    r = ref(i)
+    r["D"] = kw["D"] = None
+    if not gate:
+        r["z"] = kw["z"] = None
+    h0 = dev(i["h0"])
+    y, _ = S.wkv_scan_forward(*pos, **kw, init_state=h0)
+    got = S.wkv_scan_backward(*pos, dev(i["gy"]), **kw, init_state=h0)
+    state, one = dev(i["h0"]), [a if a.shape[0] == 24 else a[:, 5].contiguous() for a in pos]
+    y1 = S.wkv_scan_decode_step(*one, state, dt_bias=kw["dt_bias"], z=kw["z"][:, 5].contiguous() if gate else None)
+    with np.errstate(all="ignore"):
+        ry, _ = O.scan_forward(**r, init_state=i["h0"])
+        want = O.scan_backward(gy=i["gy"], init_state=i["h0"], **r)
+        tok = {k: a if a is None or k in ("A", "dt_bias") else a[:, 5:6] for k, a in r.items()}
+        r1, _ = O.scan_forward(**tok, init_state=i["h0"])
+    assert np.isinf(ry).any() and np.isinf(want["gx"]).any()
+    same(y, ry, "y")
+    same(y1, r1[:, 0], "single tokens")
+    for n, g in zip(("gx", "gdt", "gA", "gB", "gC", "gD", "gz", "gdt_bias"), got):
+        if g is not None:
+            same(g, want[n], n)
