@@ -312,11 +312,23 @@ __device__ __forceinline__ float2 scan_dot(const States<S>& a, const Row<S>& b) 
   for (int j = 0; j < S; ++j) r.n[j] = splat2(b.n[j]);
   return scan_dot<S>(a, r);
 }
-// h <- a h + s, the fold of a piece's end state.
+// h <- e^{d A} h + s, the fold of a piece's end state s; d is the sum of the
+// piece's step sizes. The decay is taken in two halves, each kept within
+// 2^-126 .. 2^127, and never formed whole: what the walk does token by token
+// then holds where it would leave float32. Nothing stays nothing under growth
+// past it, a little grows to what it does, an infinity stays one under a decay
+// that comes to 0. (A decay below 2^-252 counts as that: what it leaves of a
+// number is below 5e-38.) The backward of 1,024 pieces takes 181 us for 169
+// (B=1 T=65536 C=16), of eight pieces the same.
 template <int S>
-__device__ __forceinline__ void scan_fold(States<S>& h, const States<S>& a, const States<S>& s) {
+__device__ __forceinline__ void scan_fold(States<S>& h, float2 d, const States<S>& A2, const States<S>& s) {
+  const float2 half = mul2(d, splat2(0.5f));
 #pragma unroll
-  for (int j = 0; j < S; ++j) h.n[j] = fma2(a.n[j], h.n[j], s.n[j]);
+  for (int j = 0; j < S; ++j) {
+    const float2 x = fma2(half, A2.n[j], splat2(kEx2Low));
+    const float2 q = ex2_2(make_float2(fminf(fmaxf(x.x, -126.f), 127.f), fminf(fmaxf(x.y, -126.f), 127.f)));
+    h.n[j] = fma2(mul2(h.n[j], q), q, s.n[j]);
+  }
 }
 // One number per token of 4 tokens for each of the two channels, summed over
 // the LPC lanes of the pair: the lane ends with its first channel's sums of

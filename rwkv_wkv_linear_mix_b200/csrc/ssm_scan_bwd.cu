@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
       for (int j = w.last; j > w.seg; --j) {
         const int64_t row = ((w.b - p.whole) * p.nseg + j) * p.C + c;
         const States<S> s = ld_states<S>(p.carry + row * p.N + S * g, p.N, true, order);
-        scan_fold(q, scan_decay(make_float2(sums[row + order.swap], sums[row + 1 - order.swap]), A2), s);
+        scan_fold<S>(q, make_float2(sums[row + order.swap], sums[row + 1 - order.swap]), A2, s);
       }
     }
   }
