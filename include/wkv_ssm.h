@@ -116,10 +116,13 @@ wkv_status wkv_conv_decode_step(int64_t S, int64_t C, int dtype, int64_t W, int 
  *   q_weight, k_weight  [K] float32 or NULL (ones).
  *   eps         >= 0.
  *   inv_freq    [R/2] float32, required if R > 0.
- *   positions   DEVICE int32 [B][T] or NULL: p = pos_offset + t.
+ *   positions   DEVICE int32 [B][T] or NULL: p = pos_offset + t, which must
+ *               stay within 2^53 either way if R > 0 (else UNSUPPORTED). With
+ *               positions pos_offset is not read.
  *   q_out, k_out  like q and k; q_out = q and k_out = k (in place) is allowed.
- * Angles are reduced in 64 bits, so far positions lose nothing; the rest is
- * float32, rounded once at the end. A single token of S slots is B = S,
+ * Angles are reduced in two parts of 64 bits, so that no position loses
+ * anything; the rest is float32, rounded once at the end. The mean of squares
+ * must fit float32: entries above 1e18 overflow it. A single token of S slots is B = S,
  * T = 1 with one position per slot.
  */
 wkv_status wkv_norm_rotate(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t K, int64_t R, int dtype,

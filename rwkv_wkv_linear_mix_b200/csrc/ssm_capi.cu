@@ -168,7 +168,7 @@ WKV_EXPORT wkv_status wkv_conv_decode_step(int64_t S, int64_t C, int dtype, int6
 // ---------------------------------------------------------------------------
 
 static wkv_status check_norm(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t K, int64_t R, int dtype, float eps,
-                             int interleaved) {
+                             const int32_t* positions, int64_t pos_offset, int interleaved) {
   if (B < 0 || T < 0 || Hq < 0 || Hk < 0 || K < 0 || R < 0) return fail(WKV_ERR_INVALID_ARG, "negative size");
   if (dtype != WKV_F32 && dtype != WKV_BF16) return fail(WKV_ERR_INVALID_ARG, "unknown dtype");
   if (!(eps >= 0.f)) return fail(WKV_ERR_INVALID_ARG, "eps must be >= 0");
@@ -180,6 +180,9 @@ static wkv_status check_norm(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64
   if (T > INT32_MAX || B > INT32_MAX || Hq > 65535 || Hk > 65535) return fail(WKV_ERR_UNSUPPORTED, "size out of range");
   if (B * T > INT32_MAX || B * T > kMost / std::max<int64_t>(1, (Hq + Hk) * K))
     return fail(WKV_ERR_UNSUPPORTED, "B * T above 2^31-1 or problem above 2^40 elements");
+  constexpr int64_t kFar = (int64_t)1 << 53;  // positions that float64 holds
+  if (R > 0 && !positions && (pos_offset < -kFar || pos_offset > kFar - T))
+    return fail(WKV_ERR_UNSUPPORTED, "pos_offset + t beyond 2^53");
   return WKV_OK;
 }
 
@@ -187,7 +190,7 @@ WKV_EXPORT wkv_status wkv_norm_rotate(int64_t B, int64_t T, int64_t Hq, int64_t 
                                       const void* q, const void* k, const float* q_weight, const float* k_weight,
                                       float eps, const float* inv_freq, const int32_t* positions, int64_t pos_offset,
                                       int interleaved, void* q_out, void* k_out, void* stream) {
-  if (wkv_status s = check_norm(B, T, Hq, Hk, K, R, dtype, eps, interleaved)) return s;
+  if (wkv_status s = check_norm(B, T, Hq, Hk, K, R, dtype, eps, positions, pos_offset, interleaved)) return s;
   if (B == 0 || T == 0 || Hq + Hk == 0) return WKV_OK;
   if (Hq > 0) {
     REQUIRE_PTR(q, "q");
@@ -227,7 +230,7 @@ WKV_EXPORT wkv_status wkv_norm_rotate_backward(int64_t B, int64_t T, int64_t Hq,
                                                int64_t pos_offset, int interleaved, void* gq, void* gk,
                                                float* gq_weight, float* gk_weight, void* workspace,
                                                size_t workspace_bytes, void* stream) {
-  if (wkv_status s = check_norm(B, T, Hq, Hk, K, R, dtype, eps, interleaved)) return s;
+  if (wkv_status s = check_norm(B, T, Hq, Hk, K, R, dtype, eps, positions, pos_offset, interleaved)) return s;
   OPTIONAL_PTR(gq_weight, "gq_weight");
   OPTIONAL_PTR(gk_weight, "gk_weight");
   const bool none = B == 0 || T == 0;

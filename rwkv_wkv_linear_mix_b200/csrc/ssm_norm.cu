@@ -9,8 +9,9 @@
 // (rounded up to a power of two) per row, sums by lane exchange. A group of
 // lanes keeps its token and walks over heads, the loads of several heads in
 // flight, so that the token's sines and cosines stay in registers. They are
-// worked out once per token by the CTA: angles p * f reach 2^31 turns, so they
-// are reduced to half a turn in float64 and only then evaluated in float32.
+// worked out once per token by the CTA: positions reach 2^53, so the angle
+// p * f is reduced to half a turn in two float64 parts, and only then evaluated
+// in float32, with what the rounding of the half turn leaves added on.
 // Halves of a pair i, i + R/2 lie in lanes R/16 apart and are exchanged by
 // shuffle.
 #include "ssm_device.cuh"
@@ -43,11 +44,20 @@ __device__ __forceinline__ void norm_angles(const NormRows& a, int64_t t0, int n
     const int t = i / half, f = i - t * half;
     const int64_t tok = t0 + t;
     const int64_t p = a.positions ? (int64_t)a.positions[tok] : a.pos_offset + tok % a.T;
-    // p f / 2 pi, less its whole turns
-    double turn = (double)p * ((double)a.inv_freq[f] * 0.15915494309189535);
-    turn -= rint(turn);
+    // p f and 1 / 2 pi in two parts each, so that the turns less the whole
+    // ones are right in 64 bits, then half turns in two float32 parts
+    constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;
+    const double pd = (double)p, fd = (double)a.inv_freq[f];
+    const double angle = pd * fd, angle_low = fma(pd, fd, -angle), turns = angle * kInv;
+    const double low = fma(angle_low, kInv, fma(angle, kInvLow, fma(angle, kInv, -turns)));
+    const double half = 2.0 * ((turns - rint(turns)) + low);
+    const float h = (float)half, rest = __fmul_rn((float)(half - (double)h), 3.14159274f);
     float s, c;
-    sincospif((float)(2.0 * turn), &s, &c);
+    sincospif(h, &s, &c);
+    // turned on by the rest, below 2^-24
+    const float s1 = __fmaf_rn(c, rest, s);
+    c = __fmaf_rn(-s, rest, c);
+    s = s1;
     cs[t * row + f] = c;
     sn[t * row + f] = s;
   }
