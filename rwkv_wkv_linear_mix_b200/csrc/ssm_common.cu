@@ -6,27 +6,37 @@ namespace wkv {
 
 namespace {
 
-// Warp q of RW adds rows q, q + RW, ... in ascending order, then warp 0 adds
-// the RW warp sums in order: the result does not depend on timing.
+// Warp q of RW adds rows q, q + RW, ..., eight at a time as a tree in float32
+// and the eights in float64, then warp 0 adds the RW warp sums: in a fixed
+// order, whatever the timing. There are as many rows as sequences and more: in
+// float32 alone 2^17 like-signed ones lost 1e-4 of their sum.
 template <int RW>
 __global__ void __launch_bounds__(32 * RW) sum_rows_kernel(const SumRows s) {
   const SumRows::Plane p = s.plane[blockIdx.y];
   if ((int64_t)blockIdx.x * 32 >= p.cols) return;
-  __shared__ float sw[RW][32];
+  __shared__ double sw[RW][32];
   const int lane = threadIdx.x % 32, q = threadIdx.x / 32;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float a = 0.f;
+  double a = 0.;
   if (c < p.cols) {
-#pragma unroll 8
-    for (int64_t r = q; r < s.rows; r += RW) a = __fadd_rn(a, p.part[r * p.cols + c]);
+    for (int64_t r = q; r < s.rows; r += 8 * RW) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = r + k * RW < s.rows ? p.part[(r + k * RW) * p.cols + c] : 0.f;
+#pragma unroll
+      for (int n = 4; n > 0; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k) v[k] = __fadd_rn(v[k], v[k + n]);
+      a += (double)v[0];
+    }
   }
   sw[q][lane] = a;
   __syncthreads();
   if (q == 0 && c < p.cols) {
-    float t = sw[0][lane];
+    double t = sw[0][lane];
 #pragma unroll
-    for (int k = 1; k < RW; ++k) t = __fadd_rn(t, sw[k][lane]);
-    p.out[c] = t;
+    for (int k = 1; k < RW; ++k) t += sw[k][lane];
+    p.out[c] = (float)t;
   }
 }
 

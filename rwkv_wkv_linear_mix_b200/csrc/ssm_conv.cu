@@ -12,7 +12,8 @@
 // tokens are issued before any of them is used. The backward walks upward
 // too: token t's pre-activation gives gpre_t, which completes gx_{t-W+1}; it
 // reads W-1 tokens past the end of its run. Parameter gradients leave as one
-// partial sum per run, added in a fixed order by a second kernel.
+// partial sum per run of at most 256 tokens, added in a fixed order and in
+// float64 by a second kernel.
 #include "ssm_device.cuh"
 
 namespace wkv {
@@ -23,8 +24,9 @@ constexpr int kConvThreads = 128;
 constexpr int kConvU = 4;        // tokens whose loads are issued together, one batch ahead (forward)
 constexpr int kConvBwdU = 4;     // (backward)
 constexpr int kConvBwdN = 4;     // channels per thread of the backward
-constexpr int kConvMinRun = 16;  // tokens of a run of the forward (its last of a sequence may be shorter)
-static_assert(kConvMinRun >= 3, "only the first run may look before the sequence");
+constexpr int kConvMinRun = 16;  // tokens of a run that the forward aims at (conv_shape evens runs out, slots have as many)
+static_assert(kConvMinRun >= 3, "only the first run of a slot may look before it");
+constexpr int kConvMaxRun = 256;  // tokens whose parameter gradients are added up in one float32 chain
 template <class E>
 constexpr int kConvN = 16 / (int)sizeof(E);  // channels per thread elsewhere
 
@@ -314,13 +316,14 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(const E* __re
   }
 }
 
-ConvShape conv_shape(int64_t B, int64_t T, int64_t C, int vec, int min_run, int ctas) {
+// Runs per sequence: enough for `ctas` CTAs per SM, of about min_run tokens or
+// more (evened out, so down to half of that), and of max_run at most.
+ConvShape conv_shape(int64_t B, int64_t T, int64_t C, int vec, int min_run, int64_t max_run, int ctas) {
   ConvShape s;
   s.ncb = (int)ceil_div(C, (int64_t)kConvThreads * vec);
-  // runs per sequence: enough for that many CTAs per SM, of at least min_run tokens
   const int64_t want = ceil_div(148 * ctas, std::max<int64_t>(1, B * s.ncb));
   const int64_t most = std::max<int64_t>(1, ceil_div(T, min_run));
-  const int64_t nrun = std::max<int64_t>(1, std::min(want, most));
+  const int64_t nrun = std::max({(int64_t)1, std::min(want, most), ceil_div(T, max_run)});
   s.Lt = (int)std::max<int64_t>(1, ceil_div(T, nrun));
   s.nrun = (int)std::max<int64_t>(1, ceil_div(T, s.Lt));
   return s;
@@ -334,7 +337,7 @@ wkv_status launched(const char* what, const char** why) {
 
 template <class E, int W>
 wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
-  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, kConvMinRun, 16);
+  const ConvShape s = conv_shape(a.B, a.T, a.C, kConvN<E>, kConvMinRun, a.T, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, false> : conv_fwd_kernel<E, W, false, false>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), nullptr, static_cast<E*>(a.y), a.T, a.C, s.ncb,
@@ -344,7 +347,8 @@ wkv_status run_fwd(const ConvArgs& a, cudaStream_t st, const char** why) {
 template <class E, int W>
 wkv_status run_chunk(const ConvArgs& a, cudaStream_t st, unsigned* err, const char** why) {
   // the lengths are on the device: the runs are cut for the mean length
-  const ConvShape s = conv_shape(a.B, ceil_div(a.n_tokens, a.B), a.C, kConvN<E>, kConvMinRun, 16);
+  const int64_t mean = std::max<int64_t>(1, ceil_div(a.n_tokens, a.B));
+  const ConvShape s = conv_shape(a.B, mean, a.C, kConvN<E>, kConvMinRun, mean, 16);
   const auto kernel = a.silu ? conv_fwd_kernel<E, W, true, true> : conv_fwd_kernel<E, W, false, true>;
   kernel<<<(unsigned)(s.ncb * s.nrun * a.B), kConvThreads, 0, st>>>(
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.state), static_cast<E*>(a.state),
@@ -381,7 +385,7 @@ wkv_status run_bwd(const ConvArgs& a, cudaStream_t st, const char** why) {
 
 }  // namespace
 
-ConvShape conv_bwd_shape(int64_t B, int64_t T, int64_t C) { return conv_shape(B, T, C, kConvBwdN, 32, 16); }
+ConvShape conv_bwd_shape(int64_t B, int64_t T, int64_t C) { return conv_shape(B, T, C, kConvBwdN, 32, kConvMaxRun, 16); }
 
 wkv_status launch_conv_forward(const ConvArgs& a, cudaStream_t stream, const char** why) {
 #define CALL(E, W) (run_fwd<E, W>(a, stream, why))
