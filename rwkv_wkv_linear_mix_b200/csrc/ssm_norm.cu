@@ -23,7 +23,8 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kNormV = 8;  // elements per lane
 constexpr int kNormU = 4;     // heads whose loads are issued together (forward)
-constexpr int kNormBwdU = 4; // (backward)
+constexpr int kNormBwdU = 4;  // (backward)
+constexpr int kNormChain = 256;  // float32 additions in a row to a weight gradient (of a token's heads, if those are more)
 
 struct NormRows {
   int64_t tokens, T;
@@ -260,7 +261,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rotate_bwd_kernel(NormRo
     norm_heads_bwd<E, LR, IL>(a, q, gqo, gq, a.Hq, t0 + t, t < left, hsub, l, w[0], turn, gw[0]);
     norm_heads_bwd<E, LR, IL>(a, k, gko, gk, a.Hk, t0 + t, t < left, hsub, l, w[1], turn, gw[1]);
   }
-  // the CTA's sums: thread i < K adds element i of its RP groups in order
+  // the CTA's sums: thread i < K adds element i of its RP groups (8 or more),
+  // in eight chains of at most 32
+  static_assert(RP % 8 == 0 && RP <= 256, "eight chains");
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     __syncthreads();
@@ -268,9 +271,15 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rotate_bwd_kernel(NormRo
     for (int i = 0; i < kNormV; ++i) sums[threadIdx.x * kNormV + i] = gw[j][i];
     __syncthreads();
     if ((int)threadIdx.x < a.K) {
-      float s = 0.f;
-      for (int i = 0; i < RP; ++i) s = __fadd_rn(s, sums[i * LR * kNormV + threadIdx.x]);
-      part[((int64_t)j * gridDim.x + blockIdx.x) * a.K + threadIdx.x] = s;
+      float v[8] = {};
+      for (int i = 0; i < RP; i += 8)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = __fadd_rn(v[u], sums[(i + u) * LR * kNormV + threadIdx.x]);
+#pragma unroll
+      for (int n = 4; n > 0; n /= 2)
+#pragma unroll
+        for (int u = 0; u < n; ++u) v[u] = __fadd_rn(v[u], v[u + n]);
+      part[((int64_t)j * gridDim.x + blockIdx.x) * a.K + threadIdx.x] = v[0];
     }
   }
 }
@@ -348,9 +357,12 @@ wkv_status norm_dispatch(const NormArgs& a, bool bwd, cudaStream_t st, const cha
 
 }  // namespace
 
+// Two CTAs per SM, and as many as it takes for a group of lanes to add up no
+// more than kNormChain heads of its tokens.
 int64_t norm_bwd_blocks(int64_t tokens, int64_t Hq, int64_t Hk, int64_t K) {
-  const int64_t ntok = kNormThreads / norm_lanes(K) / norm_gpt(tokens, Hq + Hk, K);
-  return std::min<int64_t>(ceil_div(tokens, ntok), 148 * 2);
+  const int64_t gpt = norm_gpt(tokens, Hq + Hk, K), ntok = kNormThreads / norm_lanes(K) / gpt;
+  const int64_t steps = ceil_div(tokens, ntok), heads = ceil_div(std::max(Hq, Hk), gpt);  // of a token in one chain
+  return std::min(steps, std::max<int64_t>(148 * 2, ceil_div(steps, std::max<int64_t>(1, kNormChain / heads))));
 }
 
 wkv_status launch_norm_rotate(const NormArgs& a, cudaStream_t stream, const char** why) {

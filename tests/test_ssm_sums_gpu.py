@@ -60,3 +60,13 @@ def test_convolution_of_many_sequences(S, B):
     x, g = full(0.3, B, 1, C), full(0.1, B, 1, C)
     _, gw, gb, _ = S.wkv_conv_backward(x, full(0.25, W, C), g, full(0.0, C), silu=False)
     assert off(gw[1], B * f(0.3) * f(0.1)) < TOL and off(gb, B * f(0.1)) < TOL and not gw[0].any()
+
+
+def test_norm(S):
+    needs(24)
+    H, K, T = 16, 256, 606208
+    e, eps = torch.bfloat16, 0.64
+    x, g = full(1.0, 1, T, H * K, dtype=e), full(0.1, 1, T, H * K, dtype=e)
+    gq, _, gw, _ = S.wkv_norm_rotate_backward(x, None, g, None, full(1.0, K), head_size=K, eps=eps, gq=g)
+    want = T * H * float(torch.tensor(0.1, dtype=e)) / math.sqrt(1 + float(np.float32(eps)))
+    assert off(gw, want) < TOL
