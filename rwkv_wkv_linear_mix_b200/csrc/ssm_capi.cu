@@ -329,8 +329,8 @@ static ScanBwdSpace scan_bwd_space(int64_t B, int64_t T, int64_t C, int64_t N, i
     return here;
   };
   w.bc = take(2 * (size_t)scan_group_blocks(C, N, G) * B * T * G * N);
-  w.a = take((size_t)cut.rows(B) * C * N);
-  w.d = take(2 * (size_t)cut.rows(B) * C);
+  w.a = take(2 * (size_t)cut.rows(B) * C * N);  // float64
+  w.d = take(2 * 2 * (size_t)cut.rows(B) * C);
   w.carry = take((size_t)scan_carry_floats(B, C, N, cut));
   if (!has_ckpt) {
     w.ckpt = take(wkv_scan_ckpt_floats(B, T, C, N));
@@ -449,7 +449,8 @@ WKV_EXPORT wkv_status wkv_scan_backward(int64_t B, int64_t T, int64_t C, int64_t
   b.f.carry = at(w.carry);
   b.gy = gy, b.g_final = g_final, b.gx = gx, b.gdt = gdt, b.gA = gA, b.gB = gB, b.gC = gC, b.gD = gD, b.gz = z ? gz : nullptr;
   b.gdt_bias = gdt_bias, b.g_init = g_init;
-  b.part_bc = at(w.bc), b.part_a = at(w.a), b.part_d = at(w.d);
+  b.part_bc = at(w.bc);
+  b.part_a = reinterpret_cast<double*>(base + w.a), b.part_d = reinterpret_cast<double*>(base + w.d);
   return ended(launch_scan_backward(b, as_stream(stream), &why), why);
 }
 

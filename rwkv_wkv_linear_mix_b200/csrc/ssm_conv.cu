@@ -369,7 +369,7 @@ wkv_status run_bwd(const ConvArgs& a, cudaStream_t st, const char** why) {
       static_cast<const E*>(a.x), a.weight, a.bias, static_cast<const E*>(a.x_prev), static_cast<const E*>(a.gy),
       static_cast<E*>(a.gx), static_cast<E*>(a.gx_prev), a.part, a.B, a.T, a.C, s.ncb, s.nrun, s.Lt);
   if (wkv_status e = launched("conv backward kernel launch failed", why)) return e;
-  SumRows sums{};
+  SumRows<float> sums{};
   sums.rows = a.B * s.nrun;
   for (int j = 0; j <= W; ++j) sums.add(a.part + j * sums.rows * a.C, a.C, j < W ? a.gweight + j * a.C : a.gbias);
   return launch_sum_rows(sums, st, why);

@@ -11,21 +11,23 @@ namespace wkv {
 wkv_status device_error_word(unsigned** out);
 
 // For each of up to kMost planes that has an output: out[c] = the sum of
-// part[rows][cols] over its rows, in a fixed order. One launch.
+// part[rows][cols] (float or double) over its rows, in a fixed order. One launch.
+template <class P>
 struct SumRows {
   static constexpr int kMost = 5;
   struct Plane {
-    const float* part;
+    const P* part;
     int64_t cols;
     float* out;
   } plane[kMost];
   int planes;
   int64_t rows;
-  void add(const float* part, int64_t cols, float* out) {
+  void add(const P* part, int64_t cols, float* out) {
     if (out) plane[planes++] = {part, cols, out};
   }
 };
-wkv_status launch_sum_rows(const SumRows& s, cudaStream_t stream, const char** why);
+template <class P>
+wkv_status launch_sum_rows(const SumRows<P>& s, cudaStream_t stream, const char** why);
 
 // ---- short causal convolution ------------------------------------------------
 struct ConvArgs {
@@ -116,8 +118,8 @@ struct ScanBwdArgs {
   float* gdt_bias;
   float* g_init;
   float* part_bc;  // [2][blocks per group][B*T][G*N]
-  float* part_a;   // [pieces of all sequences][C][N]
-  float* part_d;   // [2][pieces of all sequences][C]: gD, gdt_bias
+  double* part_a;  // [pieces of all sequences][C][N]
+  double* part_d;  // [2][pieces of all sequences][C]: gD, gdt_bias
 };
 // State sizes the kernels are built for.
 inline int scan_padded_states(int64_t N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }

@@ -371,7 +371,7 @@ wkv_status launch_norm_rotate(const NormArgs& a, cudaStream_t stream, const char
 
 wkv_status launch_norm_rotate_backward(const NormArgs& a, cudaStream_t stream, const char** why) {
   if (wkv_status s = norm_dispatch(a, true, stream, why)) return s;
-  SumRows sums{};
+  SumRows<float> sums{};
   sums.rows = norm_bwd_blocks(a.tokens, a.Hq, a.Hk, a.K);
   sums.add(a.part, a.K, a.gwq);
   sums.add(a.part + sums.rows * a.K, a.K, a.gwk);

@@ -57,7 +57,8 @@ struct ScanParams {
   const void* gy;
   const float* g_final;
   void *gx, *gdt, *gz;
-  float *g_init, *part_bc, *part_a, *part_d;
+  float *g_init, *part_bc;
+  double *part_a, *part_d;
   // sequences that are not cut; pieces of all (here and not among the sizes,
   // where the forward takes 350 us for 345: its parameters lie worse)
   int64_t whole, rows;

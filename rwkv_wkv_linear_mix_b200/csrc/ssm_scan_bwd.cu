@@ -13,8 +13,8 @@
 // as h - d x B, which would cancel where the decay is strong. Sums over the
 // states of a channel and over the channels of a group are taken in halving
 // steps across lanes; a CTA's gB and gC leave as one partial row per token,
-// the parameter gradients as one partial row per piece, and small kernels
-// add the partial rows in a fixed order.
+// the parameter gradients as one partial row per piece (in float64, added to
+// every 256 tokens), and small kernels add the partial rows in a fixed order.
 //
 // Cut launches: the carry kernel walks every piece but the first down from
 // zero, keeping what enters the piece below (a Q at its first token) and
@@ -30,6 +30,10 @@ enum { kActX, kActDt, kActGy, kActZ, kActs };
 // Tokens whose decays and decayed states are in registers at a time, and the
 // interval of the states that a tile's first walk leaves in shared memory.
 constexpr int kBwdSub = 4;
+// Tiles whose parameter gradients are added up in float32 (256 tokens) before
+// they are added to the piece's row, in float64: one chain over a sequence of
+// 65,536 like-signed tokens lost 5e-4.
+constexpr int kBwdClose = 16;
 
 template <class E, class Geo>
 struct ScanBwdShared {
@@ -223,132 +227,151 @@ __global__ void __launch_bounds__(ScanGeom<E, LPC, S>::THREADS, scan_bwd_residen
     }
   };
 
+  // Adds the parameter gradients of up to kBwdClose tiles to the piece's row.
+  auto close = [&](bool first) {
+    if (on) {
+      double* const a = p.part_a + (w.row * p.C + c + order.swap) * p.N + S * g;
+      double* const b = p.part_a + (w.row * p.C + c + 1 - order.swap) * p.N + S * g;
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const int n = j ^ order.perm;
+        a[n] = (first ? 0. : a[n]) + (double)gA.n[j].x;
+        b[n] = (first ? 0. : b[n]) + (double)gA.n[j].y;
+        gA.n[j] = splat2(0.f);
+      }
+    }
+    // over the lanes of the channel, each of which finished other tokens
+#pragma unroll
+    for (int m = 2; m < LPC; m *= 2) {
+      gD = __fadd_rn(gD, __shfl_xor_sync(0xffffffffu, gD, m));
+      gdb = __fadd_rn(gdb, __shfl_xor_sync(0xffffffffu, gdb, m));
+    }
+    if (ch_on && g < 2) {
+      double* const d = p.part_d + w.row * p.C + c + g;
+      d[0] = (first ? 0. : d[0]) + (double)gD;
+      d[p.rows * p.C] = (first ? 0. : d[p.rows * p.C]) + (double)gdb;
+    }
+    gD = gdb = 0.f;
+  };
+
   load(nt - 1);
   States<S> h = ld_ckpt(nt - 1);
   copy_async_wait();
   __syncthreads();
-  for (int i = nt - 1; i >= 0; --i) {
-    const int64_t t0 = start(i);
-    const int left = tokens(i);
-    if (i + 1 < nt) put_sums(i + 1);
-    convert(i);
-    __syncthreads();
-    if (i > 0) load(i - 1);
-    const int64_t at = (first + t0) * p.C + c + order.swap;
-    st_h(0, h);
-    // up to the last SUB tokens, leaving the states on the way
+  for (int top = nt; top > 0; top -= kBwdClose) {
+    for (int i = top - 1; i >= max(top - kBwdClose, 0); --i) {
+      const int64_t t0 = start(i);
+      const int left = tokens(i);
+      if (i + 1 < nt) put_sums(i + 1);
+      convert(i);
+      __syncthreads();
+      if (i > 0) load(i - 1);
+      const int64_t at = (first + t0) * p.C + c + order.swap;
+      st_h(0, h);
+      // up to the last SUB tokens, leaving the states on the way
 #pragma unroll
-    for (int t = 0; t < kScanTile - SUB; ++t) {
-      const float4 dd = sm.dd[t][order.swap][pair];
-      scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), scan_taken<PAD>(dd.z, dd.w, states),
-                  ld_row<S>(&sm.B[t][order.perm][S * g]));
-      if ((t + 1) % SUB == 0 && t + 1 < kScanTile - SUB) st_h((t + 1) / SUB, h);
-    }
+      for (int t = 0; t < kScanTile - SUB; ++t) {
+        const float4 dd = sm.dd[t][order.swap][pair];
+        scan_absorb(h, scan_decay(make_float2(dd.x, dd.y), A2), scan_taken<PAD>(dd.z, dd.w, states),
+                    ld_row<S>(&sm.B[t][order.perm][S * g]));
+        if ((t + 1) % SUB == 0 && t + 1 < kScanTile - SUB) st_h((t + 1) / SUB, h);
+      }
 #pragma unroll 1
-    for (int sub = kScanTile / SUB - 1; sub >= 0; --sub) {
-      const int tb = sub * SUB;
-      if (sub < kScanTile / SUB - 1) {
-        const Row<S> a = ld_row<S>(sm.h[sub][0][tid]), b = ld_row<S>(sm.h[sub][1][tid]);
+      for (int sub = kScanTile / SUB - 1; sub >= 0; --sub) {
+        const int tb = sub * SUB;
+        if (sub < kScanTile / SUB - 1) {
+          const Row<S> a = ld_row<S>(sm.h[sub][0][tid]), b = ld_row<S>(sm.h[sub][1][tid]);
 #pragma unroll
-        for (int j = 0; j < S; ++j) h.n[j] = make_float2(a.n[j], b.n[j]);
-      }
-      // up: the decays and decayed states
-      States<S> a[SUB], ah[SUB];
-#pragma unroll
-      for (int t = 0; t < SUB; ++t) {
-        const float4 dd = sm.dd[tb + t][order.swap][pair];
-        const Row<S> Bv = ld_row<S>(&sm.B[tb + t][order.perm][S * g]);
-        a[t] = scan_decay(make_float2(dd.x, dd.y), A2);
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          ah[t].n[j] = mul2(a[t].n[j], h.n[j]);
-          h.n[j] = fma2(scan_taken<PAD>(dd.z, dd.w, states), splat2(Bv.n[j]), ah[t].n[j]);
+          for (int j = 0; j < S; ++j) h.n[j] = make_float2(a.n[j], b.n[j]);
         }
-      }
-      // down again, the states formed anew from the decayed ones (which is
-      // cheaper than to read gs and C on the way up too: the kernel is bound
-      // by what it reads of shared memory). Nothing is stored before the end
-      // of the sub-block: a store would hold back the loads behind it.
-      float gc[SUB / 2][Sums::GV], gb[SUB / 2][Sums::GV];
-      float qb[SUB], wa[SUB], s4[SUB];  // sum Q B, sum A2 Q a h, sum C h
+        // up: the decays and decayed states
+        States<S> a[SUB], ah[SUB];
 #pragma unroll
-      for (int t = SUB - 2; t >= 0; t -= 2) {
-        float rb[2][S], rc[2][S];
-#pragma unroll
-        for (int u = 1; u >= 0; --u) {
-          const int tt = tb + t + u;
-          const float4 dd = sm.dd[tt][order.swap][pair];
-          const float2 gss = sm.gs[tt][order.swap][pair], gs = scan_taken<PAD>(gss.x, gss.y, states);
-          const Row<S> Bv = ld_row<S>(&sm.B[tt][order.perm][S * g]), Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
-          const float2 d = make_float2(dd.x, dd.y), dx = scan_taken<PAD>(dd.z, dd.w, states);
-          States<S> Q, W, ht;
+        for (int t = 0; t < SUB; ++t) {
+          const float4 dd = sm.dd[tb + t][order.swap][pair];
+          const Row<S> Bv = ld_row<S>(&sm.B[tb + t][order.perm][S * g]);
+          a[t] = scan_decay(make_float2(dd.x, dd.y), A2);
 #pragma unroll
           for (int j = 0; j < S; ++j) {
-            ht.n[j] = fma2(dx, splat2(Bv.n[j]), ah[t + u].n[j]);
-            Q.n[j] = fma2(gs, splat2(Cv.n[j]), q.n[j]);
-            q.n[j] = mul2(a[t + u].n[j], Q.n[j]);
-            W.n[j] = mul2(Q.n[j], ah[t + u].n[j]);
-            gA.n[j] = fma2(d, W.n[j], gA.n[j]);
-            const float2 sb = mul2(dx, Q.n[j]), sc = mul2(gs, ht.n[j]);
-            rb[u][j] = __fadd_rn(sb.x, sb.y);
-            rc[u][j] = __fadd_rn(sc.x, sc.y);
+            ah[t].n[j] = mul2(a[t].n[j], h.n[j]);
+            h.n[j] = fma2(scan_taken<PAD>(dd.z, dd.w, states), splat2(Bv.n[j]), ah[t].n[j]);
           }
-          qb[t + u] = pair_give(scan_dot<S>(Q, Bv));
-          wa[t + u] = pair_give(scan_dot<S>(W, A2));
-          if constexpr (Z) s4[t + u] = pair_give(scan_dot<S>(ht, Cv));
         }
-        Sums::sum(rb, gb[t / 2], lane);
-        Sums::sum(rc, gc[t / 2], lane);
+        // down again, the states formed anew from the decayed ones (which is
+        // cheaper than to read gs and C on the way up too: the kernel is bound
+        // by what it reads of shared memory). Nothing is stored before the end
+        // of the sub-block: a store would hold back the loads behind it.
+        float gc[SUB / 2][Sums::GV], gb[SUB / 2][Sums::GV];
+        float qb[SUB], wa[SUB], s4[SUB];  // sum Q B, sum A2 Q a h, sum C h
+#pragma unroll
+        for (int t = SUB - 2; t >= 0; t -= 2) {
+          float rb[2][S], rc[2][S];
+#pragma unroll
+          for (int u = 1; u >= 0; --u) {
+            const int tt = tb + t + u;
+            const float4 dd = sm.dd[tt][order.swap][pair];
+            const float2 gss = sm.gs[tt][order.swap][pair], gs = scan_taken<PAD>(gss.x, gss.y, states);
+            const Row<S> Bv = ld_row<S>(&sm.B[tt][order.perm][S * g]), Cv = ld_row<S>(&sm.C[tt][order.perm][S * g]);
+            const float2 d = make_float2(dd.x, dd.y), dx = scan_taken<PAD>(dd.z, dd.w, states);
+            States<S> Q, W, ht;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+              ht.n[j] = fma2(dx, splat2(Bv.n[j]), ah[t + u].n[j]);
+              Q.n[j] = fma2(gs, splat2(Cv.n[j]), q.n[j]);
+              q.n[j] = mul2(a[t + u].n[j], Q.n[j]);
+              W.n[j] = mul2(Q.n[j], ah[t + u].n[j]);
+              gA.n[j] = fma2(d, W.n[j], gA.n[j]);
+              const float2 sb = mul2(dx, Q.n[j]), sc = mul2(gs, ht.n[j]);
+              rb[u][j] = __fadd_rn(sb.x, sb.y);
+              rc[u][j] = __fadd_rn(sc.x, sc.y);
+            }
+            qb[t + u] = pair_give(scan_dot<S>(Q, Bv));
+            wa[t + u] = pair_give(scan_dot<S>(W, A2));
+            if constexpr (Z) s4[t + u] = pair_give(scan_dot<S>(ht, Cv));
+          }
+          Sums::sum(rb, gb[t / 2], lane);
+          Sums::sum(rc, gc[t / 2], lane);
+        }
+        float out[kPairSums<LPC>], out2[kPairSums<LPC>], sv[kPairSums<LPC>];
+        pair_sums<LPC>(qb, out, lane);
+        pair_sums<LPC>(wa, out2, lane);
+        if constexpr (Z) pair_sums<LPC>(s4, sv, lane);
+        // the sub-block's results
+#pragma unroll
+        for (int t = 0; t < SUB; t += 2)
+#pragma unroll
+          for (int v = 0; v < Sums::GV; ++v) {
+            const int tt = tb + t + Sums::token(v, lane), n = S * g + ((v % Sums::GS) ^ order.perm);
+            sm.sum[1][warp][tt][n] = gc[t / 2][v];
+            sm.sum[0][warp][tt][n] = gb[t / 2][v];
+          }
+#pragma unroll
+        for (int v = 0; v < kPairSums<LPC>; ++v) {
+          const int tt = tb + pair_sum_first<LPC>(g) + v;
+          const float4 fin = sm.fin[tt][order.swap * Shared::FIN1 + pair];
+          const float d = fin.x, x = fin.y, gs = sm.gs[tt][order.swap][pair].x;
+          const float rgx = __fmaf_rn(out[v], d, p.D ? __fmul_rn(gs, D) : 0.f);  // (no product without D: gs may be infinite)
+          const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
+          if (tt < left && ch_on && g < 8) {
+            const int64_t to = at + tt * (int)p.C;
+            static_cast<E*>(p.gx)[to] = Elem<E>::from_f32(rgx);
+            static_cast<E*>(p.gdt)[to] = Elem<E>::from_f32(graw);
+            if constexpr (Z)
+              static_cast<E*>(p.gz)[to] = Elem<E>::from_f32(__fmul_rn(fin.w, p.D ? __fmaf_rn(D, x, sv[v]) : sv[v]));
+            gD = __fmaf_rn(gs, x, gD);
+            gdb = __fadd_rn(gdb, graw);
+          }
+        }
       }
-      float out[kPairSums<LPC>], out2[kPairSums<LPC>], sv[kPairSums<LPC>];
-      pair_sums<LPC>(qb, out, lane);
-      pair_sums<LPC>(wa, out2, lane);
-      if constexpr (Z) pair_sums<LPC>(s4, sv, lane);
-      // the sub-block's results
-#pragma unroll
-      for (int t = 0; t < SUB; t += 2)
-#pragma unroll
-        for (int v = 0; v < Sums::GV; ++v) {
-          const int tt = tb + t + Sums::token(v, lane), n = S * g + ((v % Sums::GS) ^ order.perm);
-          sm.sum[1][warp][tt][n] = gc[t / 2][v];
-          sm.sum[0][warp][tt][n] = gb[t / 2][v];
-        }
-#pragma unroll
-      for (int v = 0; v < kPairSums<LPC>; ++v) {
-        const int tt = tb + pair_sum_first<LPC>(g) + v;
-        const float4 fin = sm.fin[tt][order.swap * Shared::FIN1 + pair];
-        const float d = fin.x, x = fin.y, gs = sm.gs[tt][order.swap][pair].x;
-        const float rgx = __fmaf_rn(out[v], d, p.D ? __fmul_rn(gs, D) : 0.f);  // (no product without D: gs may be infinite)
-        const float graw = __fmul_rn(__fmaf_rn(out[v], x, __fmul_rn(out2[v], 1.f / kLog2e)), fin.z);
-        if (tt < left && ch_on && g < 8) {
-          const int64_t to = at + tt * (int)p.C;
-          static_cast<E*>(p.gx)[to] = Elem<E>::from_f32(rgx);
-          static_cast<E*>(p.gdt)[to] = Elem<E>::from_f32(graw);
-          if constexpr (Z)
-            static_cast<E*>(p.gz)[to] = Elem<E>::from_f32(__fmul_rn(fin.w, p.D ? __fmaf_rn(D, x, sv[v]) : sv[v]));
-          gD = __fmaf_rn(gs, x, gD);
-          gdb = __fadd_rn(gdb, graw);
-        }
-      }
+      if (i > 0) h = ld_ckpt(i - 1);
+      copy_async_wait();
+      __syncthreads();
     }
-    if (i > 0) h = ld_ckpt(i - 1);
-    copy_async_wait();
-    __syncthreads();
+    close(top == nt);
   }
   put_sums(0);
 
-  if (on) st_states<S>(p.part_a + (w.row * p.C + c) * p.N + S * g, p.N, gA, order);
   if (on && p.g_init && w.seg == 0) st_states<S>(p.g_init + state_at, p.N, q, order);
-  // over the lanes of the channel, each of which finished other tokens
-#pragma unroll
-  for (int m = 2; m < LPC; m *= 2) {
-    gD = __fadd_rn(gD, __shfl_xor_sync(0xffffffffu, gD, m));
-    gdb = __fadd_rn(gdb, __shfl_xor_sync(0xffffffffu, gdb, m));
-  }
-  if (ch_on && g < 2) {
-    p.part_d[w.row * p.C + c + g] = gD;
-    p.part_d[(p.rows + w.row) * p.C + c + g] = gdb;
-  }
 }
 
 // What a piece, walked down from Q = 0, hands to the piece below, and its sum of d.
@@ -497,7 +520,7 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
   scan_sum_bc_kernel<E><<<dim3((unsigned)ceil_div(n4, 256), 2), 256, 0, st>>>(b.part_bc, p.nbg, n4, static_cast<E*>(b.gB),
                                                                             static_cast<E*>(b.gC));
   if (wkv_status s = launched("scan gB, gC sum kernel launch failed", why)) return s;
-  SumRows sums{};
+  SumRows<double> sums{};
   sums.rows = cut.rows(a.B);
   sums.add(b.part_a, a.C * a.N, b.gA);
   sums.add(b.part_d, a.C, b.gD);
