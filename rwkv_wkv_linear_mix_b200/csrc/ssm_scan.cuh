@@ -350,22 +350,21 @@ __device__ __forceinline__ void pair_sums(float (&v)[4], float (&out)[kPairSums<
   for (int t = 0; t < kPairSums<LPC>; ++t) out[t] = v[t];
 }
 
-// Host: the sequences from `whole` on in at most nseg pieces, each of at least
-// 4 tiles.
+// Host: the sequences from `whole` on in at most nseg pieces of the same length
+// (4 tiles or more), but for the last, which takes what is left.
 inline ScanCut scan_cut(int64_t B, int64_t whole, int64_t nseg, int64_t T) {
   const int64_t tiles = std::max<int64_t>(1, ceil_div(T, kScanTile));
   const int64_t per = ceil_div(tiles, std::max<int64_t>(1, std::min(nseg, tiles / 4)));
   const int64_t n = ceil_div(tiles, per);
   return ScanCut{n > 1 ? whole : B, (int)n, (int)per};
 }
-// A launch with `ctas` CTAs per sequence. With fewer than two per SM in all,
-// every sequence is cut for about eight per SM, which is what an SM holds
-// (four: 205 against 176 us at B=1 T=8191 C=1536); else none is, since the
-// carry pass costs most of a second walk (B=2 C=4096, 256 CTAs, cut and uncut:
-// 217 and 209 us forward, 502 and 522 backward; B=4: 387 and 303, 921 and 852).
-inline ScanCut scan_cut_few(int64_t B, int64_t ctas, int64_t T) {
+// A launch with `ctas` CTAs per sequence. With fewer than `few` in all, every
+// sequence is cut for about eight per SM, which is what an SM holds (four: 205
+// against 176 us at B=1 T=8191 C=1536); else none is, since the carry pass costs
+// most of a second walk.
+inline ScanCut scan_cut_few(int64_t B, int64_t ctas, int64_t T, int64_t few) {
   const int64_t all = std::max<int64_t>(1, B * ctas);
-  return all < 148 * 2 ? scan_cut(B, 0, ceil_div(148 * 8, all), T) : scan_cut(B, B, 1, T);
+  return all < few ? scan_cut(B, 0, ceil_div(148 * 8, all), T) : scan_cut(B, B, 1, T);
 }
 
 // Host: the parameters a launch has in common.

@@ -536,14 +536,22 @@ wkv_status run_backward(const ScanBwdArgs& b, cudaStream_t st, const char** why)
 // what their carry pass takes, about a quarter of their walk (T=2048 C=2560,
 // 640 CTAs: 1044 -> 900 us at B=8; 960 CTAs: 706 -> 681; where all fit at
 // once it does not pay: 384 CTAs, 652 -> 737).
+// A launch of few CTAs is cut altogether, up to where the two cross. Cut and
+// uncut, us, by CTAs (bf16, N=8 f32):
+//          N=8 T=2048   N=16 T=2048   N=32 T=2048   N=64 T=2048
+//   192     552 / 649     363 / 498     650 / 778     680 / 820
+//   224     640 / 656     428 / 502     757 / 783     790 / 826
+//   256     730 / 662     479 / 506     829 / 786     878 / 831
+//   288     782 / 668     522 / 511     915 / 792     966 / 838
 ScanCut scan_bwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
   const int64_t ctas = G * scan_group_blocks(C, N, G), all = B * ctas;
-  if (all > 148 * scan_bwd_resident(scan_padded_states(N) <= 16 ? 2 : 4)) {
+  const int states = scan_padded_states(N);
+  if (all > 148 * scan_bwd_resident(states <= 16 ? 2 : 4)) {
     const int64_t whole = all / 148 * 148 / ctas;
     const double idle = 1. - (double)all / (double)(148 * ceil_div(all, 148));
     if (idle > 0.25 * (double)(B - whole) / (double)B) return scan_cut(B, whole, 8, T);
   }
-  return scan_cut_few(B, ctas, T);
+  return scan_cut_few(B, ctas, T, states == 16 ? 148 * 9 / 5 : 148 * 5 / 3);
 }
 
 wkv_status launch_scan_backward(const ScanBwdArgs& a, cudaStream_t stream, const char** why) {

@@ -335,8 +335,15 @@ wkv_status run_decode(const ScanArgs& a, cudaStream_t st, const char** why) {
 
 }  // namespace
 
+// Cut with fewer than three CTAs for two SMs, about where the two cross. Cut and
+// uncut, us, by CTAs (bf16, N=8 f32):
+//         N=8 T=2048   N=16 T=512   N=16 T=2048   N=16 T=8192   N=32 T=2048   N=64 T=2048
+//   128    150 / 205     35 / 41     110 / 154     399 / 605     175 / 205     169 / 191
+//   192    210 / 239     49 / 49     156 / 182     584 / 708     251 / 263     243 / 253
+//   224    244 / 239     56 / 49     179 / 182     680 / 708     292 / 262     283 / 254
+//   256    271 / 239     60 / 49     193 / 183     731 / 710     316 / 263     304 / 253
 ScanCut scan_fwd_cut(int64_t B, int64_t T, int64_t C, int64_t N, int64_t G) {
-  return scan_cut_few(B, G * scan_group_blocks(C, N, G), T);
+  return scan_cut_few(B, G * scan_group_blocks(C, N, G), T, 148 * 3 / 2);
 }
 
 wkv_status launch_scan_forward(const ScanArgs& a, cudaStream_t stream, const char** why) {

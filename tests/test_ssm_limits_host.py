@@ -31,3 +31,12 @@ def test_positions_beyond_what_float64_holds(L):
             assert f(offset) == 1 and b"q is NULL" in L.wkv_last_error()
     assert forward(far, R=0) == 1 and b"q is NULL" in L.wkv_last_error()             # nothing turns
     assert forward(far, positions=FAKE) == 1 and b"q is NULL" in L.wkv_last_error()  # not read
+
+
+def test_launches_cut_along_T(L):
+    """Few CTAs (32 channels each at N = 16) are cut, those that fill the SMs
+    are not: fewer than three for two SMs in the forward."""
+    ws = L.wkv_scan_forward_workspace_bytes
+    assert ws(1, 4096, 32 * 221, 16, 1) > 0 and ws(1, 4096, 32 * 222, 16, 1) == 0
+    assert ws(2, 2048, 4096, 16, 1) == 0 and ws(2, 2048, 2560, 16, 1) > 0
+    assert ws(1, 64, 64, 16, 1) == 0  # too short to cut
