@@ -201,11 +201,13 @@ def wkv_conv_decode_step(x, weight, state: torch.Tensor, bias=None, *, silu: boo
 # per-head norm with position rotation
 # ----------------------------------------------------------------------------
 
-def _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, K):
+def _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, K, pos_offset):
     """(device, dtype, dtype code, sizes B T Hq Hk K R, the addresses of the
     operands) of a call; q or k may be None."""
     if K < 1:
         raise ValueError("head_size must be at least 1")
+    if not -(1 << 63) <= pos_offset < 1 << 63:
+        raise ValueError("pos_offset must fit 64 bits")
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q and k are both None")
@@ -240,8 +242,9 @@ def wkv_norm_rotate(q, k, q_weight=None, k_weight=None, inv_freq=None, positions
     2 * len(inv_freq) entries by position, in one pass. q: [B, T, Hq*K], k:
     [B, T, Hk*K] (either may be None); q_weight, k_weight: [K] float32;
     inv_freq: [R/2] float32 (None: no rotation); positions: int32 [B, T] (None:
-    pos_offset + t). q_out=q and k_out=k work in place. Returns (q_out, k_out)."""
-    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, head_size)
+    pos_offset + t, within 2^53). q_out=q and k_out=k work in place. Returns (q_out, k_out)."""
+    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(
+        q, k, q_weight, k_weight, inv_freq, positions, head_size, pos_offset)
     qo = ko = None
     if q is not None:
         q_out, qo = _like(q, q_out, "q_out", e, q.shape, dev)
@@ -257,7 +260,8 @@ def wkv_norm_rotate_backward(q, k, gq_out, gk_out, q_weight=None, k_weight=None,
     """Gradients of sum(gq_out * q_out) + sum(gk_out * k_out) for wkv_norm_rotate
     with the same arguments. Returns (gq, gk, gq_weight, gk_weight); a weight's
     gradient is None where there is no such weight."""
-    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(q, k, q_weight, k_weight, inv_freq, positions, head_size)
+    dev, e, code, sizes, (qp, kp, wq, wk, fr, po) = _norm_operands(
+        q, k, q_weight, k_weight, inv_freq, positions, head_size, pos_offset)
     gop = kop = gqp = gkp = gwqp = gwkp = gwq = gwk = None
     if q is not None:
         gop = _has(gq_out, "gq_out", e, q.shape, dev)

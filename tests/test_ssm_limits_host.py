@@ -40,3 +40,12 @@ def test_launches_cut_along_T(L):
     assert ws(1, 4096, 32 * 221, 16, 1) > 0 and ws(1, 4096, 32 * 222, 16, 1) == 0
     assert ws(2, 2048, 4096, 16, 1) == 0 and ws(2, 2048, 2560, 16, 1) > 0
     assert ws(1, 64, 64, 16, 1) == 0  # too short to cut
+
+
+@pytest.mark.parametrize("offset", [1 << 63, (1 << 64) + 5, -(1 << 63) - 1])
+def test_an_offset_past_64_bits_is_not_wrapped(L, offset):
+    from rwkv_wkv_linear_mix_b200 import ssm
+    for f in (lambda: ssm.wkv_norm_rotate(None, None, head_size=8, pos_offset=offset),
+              lambda: ssm.wkv_norm_rotate_backward(None, None, None, None, head_size=8, pos_offset=offset)):
+        with pytest.raises(ValueError, match="64 bits"):
+            f()
