@@ -124,7 +124,7 @@ wkv_status wkv_conv_decode_step(int64_t S, int64_t C, int dtype, int64_t W, int 
  *               positions pos_offset is not read.
  *   q_out, k_out  like q and k; q_out = q and k_out = k (in place) is allowed.
  * Angles are reduced in two parts of 64 bits, so that no position loses
- * anything; the rest is float32, rounded once at the end. The mean of squares
+ * anything (up to angles of 2^65); the rest is float32, rounded once at the end. The mean of squares
  * must fit float32: entries above 1e18 overflow it. A single token of S slots is B = S,
  * T = 1 with one position per slot.
  */

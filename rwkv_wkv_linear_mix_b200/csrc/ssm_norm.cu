@@ -51,7 +51,7 @@ __device__ __forceinline__ void norm_angles(const NormRows& a, int64_t t0, int n
     const double pd = (double)p, fd = (double)a.inv_freq[f];
     const double angle = pd * fd, angle_low = fma(pd, fd, -angle), turns = angle * kInv;
     const double low = fma(angle_low, kInv, fma(angle, kInvLow, fma(angle, kInv, -turns)));
-    const double half = 2.0 * ((turns - rint(turns)) + low);
+    const double half = 2.0 * ((turns - rint(turns)) + (low - rint(low)));  // from 2^53 turns on low has whole ones
     const float h = (float)half, rest = __fmul_rn((float)(half - (double)h), 3.14159274f);
     float s, c;
     sincospif(h, &s, &c);

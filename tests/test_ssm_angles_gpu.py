@@ -61,3 +61,29 @@ def test_gradient_turns_back_by_the_same_angle(S):
                                              inv_freq=torch.ones(8, device="cuda"),
                                              positions=torch.tensor([p[3:4]], dtype=torch.int32).cuda(), head_size=16, eps=0.0)
     assert abs(gw[0].item() / np.sin(355.0) - 1) < TOL and abs(gw[8].item() / np.cos(355.0) - 1) < TOL
+
+
+def turned(S, offset, freq):
+    q = torch.zeros(1, 64, 16, device="cuda")
+    q[..., 0] = 1.0
+    out, _ = S.wkv_norm_rotate(q, None, inv_freq=torch.full((8,), freq, device="cuda"), pos_offset=offset, head_size=16, eps=0.0)
+    got = out[0].double().cpu().numpy() / 4
+    return got[:, 0], got[:, 8]
+
+
+@pytest.mark.parametrize("offset,freq", [(2 ** 31 + 5, 4096.0), (2 ** 53 - 64, 8.0), (-(2 ** 53), 2.0 ** 12)])
+def test_far_offsets_at_high_frequencies(S, offset, freq):
+    """Angles of up to 2^65 (whole numbers of 53 bits, so that float64 holds
+    them): more turns than float64 counts one by one. 1 / 2 pi in two parts is
+    right to 2^-109, so the turns to 2^-44."""
+    angle = np.array([float(offset + t) * freq for t in range(64)])
+    for g, w in zip(turned(S, offset, freq), (np.cos(angle), np.sin(angle))):
+        assert (np.abs(g - w) / np.abs(w)).max() < TOL
+
+
+def test_a_turn_stays_a_turn(S):
+    """At frequencies whose angles no one can know, (1, 0) still goes to a
+    point of the unit circle."""
+    for freq in (2.0 ** 40, 3e38):
+        c, s = turned(S, 2 ** 53 - 64, freq)
+        assert np.abs(c * c + s * s - 1).max() < 2 * TOL
