@@ -124,9 +124,10 @@ wkv_status wkv_conv_decode_step(int64_t S, int64_t C, int dtype, int64_t W, int 
  *               positions pos_offset is not read.
  *   q_out, k_out  like q and k; q_out = q and k_out = k (in place) is allowed.
  * Angles are reduced in two parts of 64 bits, so that no position loses
- * anything (up to angles of 2^65); the rest is float32, rounded once at the end. The mean of squares
- * must fit float32: entries above 1e18 overflow it. A single token of S slots is B = S,
- * T = 1 with one position per slot.
+ * anything (up to angles of 2^65); the rest is float32, rounded once at the
+ * end. The mean of squares must fit float32: entries above 1e18 overflow it,
+ * and with eps = 0 a head below 1e-19 is lost to it. A single token of S slots
+ * is B = S, T = 1 with one position per slot.
  */
 wkv_status wkv_norm_rotate(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t K, int64_t R, int dtype,
                            const void *q, const void *k, const float *q_weight, const float *k_weight,
