@@ -26,7 +26,9 @@ constexpr int kConvBwdU = 4;     // (backward)
 constexpr int kConvBwdN = 4;     // channels per thread of the backward
 constexpr int kConvMinRun = 16;  // tokens of a run that the forward aims at (conv_shape evens runs out, slots have as many)
 static_assert(kConvMinRun >= 3, "only the first run of a slot may look before it");
-constexpr int kConvMaxRun = 256;  // tokens whose parameter gradients are added up in one float32 chain
+// Tokens whose parameter gradients are added up in one float32 chain (32,768
+// like-signed ones lost 4e-4 of the sum; 3e-6 now).
+constexpr int kConvMaxRun = 256;
 template <class E>
 constexpr int kConvN = 16 / (int)sizeof(E);  // channels per thread elsewhere
 

@@ -7,7 +7,7 @@ Tolerance. At most 256 additions in a row are in float32, each off by at most
 sign). The addends' own error: a state that remembers one or two tokens and
 four factors, ten times 2^-23 = 1.2e-6; the sum over lanes and the result's
 rounding, five times 2^-24. Together 9.2e-6, held to 1.2e-5. (One chain over
-the sequences here is off by 5e-5 to 5e-4.)"""
+the sequences here is off by 3e-5 to 6e-4.)"""
 
 import math
 
